@@ -33,6 +33,11 @@
  *    positions (a prompt chunk computed against a longer cache).
  *  - *_dir: the same calls over a two-level page map sized to the pages in
  *    use (SPIN's two-level metadata).
+ *  - sa_append_kv_rope: packed new tokens appended with the rotary position
+ *    rotation applied on the way (keys and queries), summaries refreshed.
+ *  - sa_chunk_attention: exact attention of packed new tokens over the whole
+ *    paged cache (decode tokens, drafts, prompt chunks, mixed).
+ *  - sa_prompt_attention: exact causal attention over whole packed prompts.
  *
  * Conventions for every call:
  *  - Pointers marked (dev) are caller-owned device memory on the current
@@ -609,6 +614,146 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
                             const int32_t* seq_lens, int32_t* out_seq_lens, int B, int Hkv,
                             int D, int page_size, int P_pool, uint16_t* summaries,
                             int32_t* dev_error, void* stream);
+
+/*
+ * Packed batches.  The three operators below take the new tokens of a batch
+ * end to end: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 (n_b of them,
+ * any number, none included) of [tokens, heads, D] tensors, cu being B + 1
+ * non-decreasing device int32 offsets with cu[0] >= 0 and cu[B] <= the number
+ * of tokens the call is given.  Tokens behind cu[B] are neither read nor
+ * written.  An offset that breaks this is flagged (SA_DEVERR_COUNT): the
+ * attention calls then hold it inside the tensors (what such a sequence's rows
+ * receive is unspecified), the append skips the sequence.
+ * Strides are three (token, head, feature), with the rules of every bf16
+ * tensor (feature 1, the others multiples of 8, base 16-byte aligned).
+ */
+
+/*
+ * sa_append_kv_rope — append packed new tokens to the paged cache, rotating
+ * keys (and queries) by their positions on the way, and refresh the summaries
+ * of the pages they land in, in one launch.
+ *
+ * Token i of sequence b sits at position p = seq_lens[b] + i.  With r =
+ * rot_dim, c_k = rope_table[p, k] and s_k = rope_table[p, r/2 + k] (k < r/2),
+ * each head's features are rotated in pairs (x_i, x_j) -> (x_i c_k - x_j s_k,
+ * x_j c_k + x_i s_k), where (i, j) = (k, k + r/2), or (2k, 2k + 1) when
+ * `interleaved`; features past r are copied.  Every product and sum is rounded
+ * to float32 and the result once to bf16.  The rotated key goes to row p % P
+ * of page page_table[b, p / P], the value beside it unrotated, the rotated
+ * query to q_out.  Then, for every page the tokens fall in, summaries[page, g]
+ * becomes the mean of the page's stored keys at positions below seq_lens[b] +
+ * n_b, as sa_build_page_summaries computes it.  No other row changes.
+ * Positions past the page table's row or at or past n_pos are dropped and
+ * flagged (SA_DEVERR_PAGE_RANGE; a query past n_pos is not written either);
+ * tokens whose page id is out of range likewise (SA_DEVERR_POOL_RANGE).
+ *
+ *  q_new      (dev, optional) [total_new,Hq,D] bf16; NULL: no queries
+ *  k_new, v_new (dev) [total_new,Hkv,D] bf16
+ *  cu_new     (dev) [B+1] int32
+ *  rope_table (dev) [n_pos,rot_dim] float32, contiguous, 16-byte aligned:
+ *             cosines, then sines (NULL when rot_dim == 0: a plain append)
+ *  q_out      (dev) [total_new,Hq,D] bf16, contiguous; may be q_new itself
+ *  k_out      (dev, optional) [total_new,Hkv,D] bf16, contiguous: the rotated
+ *             keys, packed (for sa_prompt_attention); may be k_new itself
+ *  k_cache, v_cache (dev) [P_pool,Hkv,P,D] bf16, written in place
+ *  seq_lens   (dev) [B] int32: the lengths BEFORE the append
+ *  out_seq_lens (dev, optional) [B] int32: receives seq_lens[b] + n_b; must not
+ *             be seq_lens itself
+ *  summaries  (dev, optional) [P_pool,Hkv,D] bf16, contiguous
+ * D % 8 == 0, D <= 256; rot_dim % 16 == 0, rot_dim <= D.  Appends that touch
+ * the same page from two sequences race.
+ */
+SA_API int sa_append_kv_rope(const uint16_t* q_new, const int64_t q_strides[3],
+                             const uint16_t* k_new, const int64_t kn_strides[3],
+                             const uint16_t* v_new, const int64_t vn_strides[3],
+                             const int32_t* cu_new, int total_new, const float* rope_table,
+                             int n_pos, int rot_dim, int interleaved, uint16_t* q_out,
+                             uint16_t* k_out, uint16_t* k_cache, const int64_t k_strides[4],
+                             uint16_t* v_cache, const int64_t v_strides[4],
+                             const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                             int32_t* out_seq_lens, int B, int Hq, int Hkv, int D, int page_size,
+                             int P_pool, uint16_t* summaries, int32_t* dev_error, void* stream);
+SA_API int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[3],
+                                 const uint16_t* k_new, const int64_t kn_strides[3],
+                                 const uint16_t* v_new, const int64_t vn_strides[3],
+                                 const int32_t* cu_new, int total_new, const float* rope_table,
+                                 int n_pos, int rot_dim, int interleaved, uint16_t* q_out,
+                                 uint16_t* k_out, uint16_t* k_cache, const int64_t k_strides[4],
+                                 uint16_t* v_cache, const int64_t v_strides[4],
+                                 const int32_t* page_dir, int n_dir, const int32_t* page_blocks,
+                                 int n_blocks, int block_shift, const int32_t* seq_lens,
+                                 int32_t* out_seq_lens, int B, int Hq, int Hkv, int D,
+                                 int page_size, int P_pool, uint16_t* summaries,
+                                 int32_t* dev_error, void* stream);
+
+/*
+ * sa_chunk_attention — exact attention of packed new tokens over the whole
+ * paged cache: single decode tokens, draft tokens, prompt chunks, or a mix in
+ * one call.  The cache already holds the new tokens' keys and values
+ * (sa_append_kv_rope, sa_append_kv) and seq_lens counts them: query token i of
+ * sequence b sits at position p = seq_lens[b] - n_b + i and sees the keys j <=
+ * p, j < seq_lens[b] and, when window > 0, j > p - window (the last `window`
+ * keys, its own among them).  S_j = scale * q.k_j, O = softmax(S) V, lse = ln
+ * sum exp S; a row that sees no key gives O = 0, lse = -inf.
+ *
+ *  q          (dev) [total_q,Hq,D] bf16;  cu_q (dev) [B+1] int32
+ *  k_cache, v_cache (dev) [P_pool,Hkv,P,D] bf16, strides as sa_sparse_decode
+ *  page_table (dev) [B,max_pages] int32;  seq_lens (dev) [B] int32
+ *  scale      finite, above 0
+ *  window     0 (every earlier key) or the number of keys a token sees
+ *  o_out      (dev) [total_q,Hq,D] bf16, contiguous, 16-byte aligned
+ *  lse_out    (dev, optional) [total_q,Hq] float32
+ *  workspace  (dev) sa_dense_attention_workspace_size(total_q,Hq,Hkv,D) bytes,
+ *             16-byte aligned, caller-owned, no initial contents; calls (or
+ *             captured graphs) sharing one must not overlap
+ * Probabilities enter the value product as bf16 (one rounding each); sums, the
+ * softmax statistics and the LSE are float32.  Keys and values past a
+ * sequence's end may hold anything; the sequence's own must be finite.  Keys on
+ * a page whose id is out of range are left out (SA_DEVERR_POOL_RANGE); a
+ * seq_len outside the page map is held inside it (SA_DEVERR_PAGE_RANGE).
+ * The result does not depend on timing: the same call gives the same bits on
+ * the same kind of device.
+ * Supported: D in {64,128}, page_size a multiple of 16, Hq/Hkv <= 128, B <=
+ * 4096, total_q * Hq < 2^30, max_pages * page_size < 2^30 (SA_ERR_UNSUPPORTED
+ * otherwise).  Two launches (the second merges parts of items that were split
+ * between SMs).
+ */
+SA_API size_t sa_dense_attention_workspace_size(int total_q, int Hq, int Hkv, int D);
+SA_API int sa_chunk_attention(const uint16_t* q, const int64_t q_strides[3], const int32_t* cu_q,
+                              int total_q, const uint16_t* k_cache, const int64_t k_strides[4],
+                              const uint16_t* v_cache, const int64_t v_strides[4],
+                              const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                              int B, int Hq, int Hkv, int D, int page_size, int P_pool,
+                              float scale, int window, uint16_t* o_out, float* lse_out,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                              void* stream);
+SA_API int sa_chunk_attention_dir(const uint16_t* q, const int64_t q_strides[3],
+                                  const int32_t* cu_q, int total_q, const uint16_t* k_cache,
+                                  const int64_t k_strides[4], const uint16_t* v_cache,
+                                  const int64_t v_strides[4], const int32_t* page_dir, int n_dir,
+                                  const int32_t* page_blocks, int n_blocks, int block_shift,
+                                  const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                                  int page_size, int P_pool, float scale, int window,
+                                  uint16_t* o_out, float* lse_out, void* workspace,
+                                  size_t workspace_bytes, int32_t* dev_error, void* stream);
+
+/*
+ * sa_prompt_attention — sa_chunk_attention over packed keys and values that are
+ * in no cache: whole prompts of different lengths, causal, grouped heads.
+ * Sequence b's keys are the tokens cu_k[b] .. cu_k[b + 1] - 1 of k and v (L_b
+ * of them; normally cu_k is cu_q), and its query token i sits at position L_b -
+ * n_b + i.  Everything else as sa_chunk_attention.
+ *
+ *  k, v       (dev) [total_k,Hkv,D] bf16;  cu_k (dev) [B+1] int32
+ * total_k < 2^30.
+ */
+SA_API int sa_prompt_attention(const uint16_t* q, const int64_t q_strides[3], const int32_t* cu_q,
+                               int total_q, const uint16_t* k, const int64_t k_strides[3],
+                               const uint16_t* v, const int64_t v_strides[3],
+                               const int32_t* cu_k, int total_k, int B, int Hq, int Hkv, int D,
+                               float scale, int window, uint16_t* o_out, float* lse_out,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                               void* stream);
 
 /*
  * sa_block_union — per-group KV block tables for chunked prefill.

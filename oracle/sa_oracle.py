@@ -47,6 +47,13 @@ Readings where the pages are silent (each also listed in the design notes):
      K and V pages stored as FP8 E4M3 codes with one float32 scale per
      (physical page, kv head); a key is e4m3(code) * scale, likewise a value.
      Attention and summaries are those of the dequantized pages.
+  R20 rotary positions: features (x_i, x_j) of pair k of a head at position p
+     become (x_i c - x_j s, x_j c + x_i s) with c = table[p, k], s =
+     table[p, r/2 + k]; (i, j) = (k, k + r/2), or (2k, 2k + 1) interleaved;
+     every product and sum rounded to float32, the result once to bf16.
+  R21 dense attention of packed tokens: token i of the n of a sequence of L
+     keys sits at position L - n + i and sees the keys at or before it (with a
+     window, the last `window` of them); no visible key: O = 0, LSE = -inf.
   R19 two-level page map ([SPIN] abstract on the page titled "Vortex:
      Efficient and Programmable Sparse Attention Serving for AI Agents": page
      metadata in two levels sized to the working set): a directory
@@ -68,6 +75,7 @@ __all__ = [
     "select_pages_mla", "sparse_attention", "sparse_attention_fp8", "masked_dense_attention",
     "combine", "block_union", "append_kv", "ambient_head_scores", "select_ambient_heads",
     "page_table_from_dir", "NEG_INF",
+    "rotate_bf16", "append_kv_rope", "dense_attention",
 ]
 
 NEG_INF = float("-inf")
@@ -645,3 +653,75 @@ def select_ambient_heads(q_bits, sig_bits, page_table, seq_lens, crit_lists, cri
     heads = np.arange(len(sc))
     win = rank_select(sc, heads, h)
     return heads[win].astype(np.int32), sc
+
+
+# --------------------------------------------------------------------------
+# R20, R21: packed batches -- rotated appends and dense attention
+# --------------------------------------------------------------------------
+def rotate_bf16(x_bits, table, positions, interleaved: bool = False) -> np.ndarray:
+    """x_bits [n, H, D] bf16 bits at integer positions [n]; table [n_pos, r] float32
+    (cosines, then sines) -> rotated bf16 bits, float32 arithmetic throughout."""
+    x = (np.asarray(x_bits, dtype=np.uint16).astype(np.uint32) << 16).view(np.float32)
+    t = np.asarray(table, dtype=np.float32)[np.asarray(positions, dtype=np.int64)]
+    r = t.shape[1]
+    c, s = t[:, None, :r // 2], t[:, None, r // 2:]
+    i = np.arange(0, r, 2) if interleaved else np.arange(r // 2)
+    j = i + 1 if interleaved else i + r // 2
+    out = x.copy()
+    a, b = x[..., i], x[..., j]
+    out[..., i] = a * c - b * s
+    out[..., j] = b * c + a * s
+    bits = f64_to_bf16_rne(out.astype(np.float64))
+    return np.where(np.arange(x.shape[-1]) < r, bits, np.asarray(x_bits, dtype=np.uint16))
+
+
+def append_kv_rope(q_bits, k_bits, v_bits, cu, table, k_cache, v_cache, sig_bits, page_table,
+                   seq_lens, page_size: int, interleaved: bool = False):
+    """New pools, summaries and lengths and the rotated queries and keys after sequence b
+    appends the packed tokens cu[b] .. cu[b + 1] - 1; q_bits [n, Hq, D], k_bits and v_bits
+    [n, Hkv, D].  table None: no rotation."""
+    cu = np.asarray(cu, dtype=np.int64)
+    sl = np.asarray(seq_lens, dtype=np.int64)
+    nn = np.diff(cu)
+    B, Hkv, D = len(sl), k_bits.shape[1], k_bits.shape[2]
+    pos = np.concatenate([sl[b] + np.arange(nn[b]) for b in range(B)]).astype(np.int64)
+    if table is None:
+        table = np.zeros((1, 0), dtype=np.float32)
+        q_rot, k_rot = np.array(q_bits), np.array(k_bits)
+    else:
+        q_rot = rotate_bf16(q_bits[cu[0]:cu[-1]], table, pos, interleaved)
+        k_rot = rotate_bf16(k_bits[cu[0]:cu[-1]], table, pos, interleaved)
+    m = int(nn.max(initial=0))
+    kn, vn = (np.zeros((B, m, Hkv, D), dtype=np.uint16) for _ in range(2))
+    for b in range(B):
+        kn[b, :nn[b]] = k_rot[cu[b] - cu[0]:cu[b + 1] - cu[0]]
+        vn[b, :nn[b]] = v_bits[cu[b]:cu[b + 1]]
+    k2, v2, s2, new = append_kv(k_cache, v_cache, sig_bits, page_table, seq_lens, kn, vn, nn,
+                                page_size)
+    return q_rot, k_rot, k2, v2, s2, new
+
+
+def dense_attention(q, k, v, scale: float, window: int = 0):
+    """One sequence, float64: q [n, Hq, D], k and v [L, Hkv, D] -> (O [n, Hq, D], lse [n, Hq],
+    A [n, Hq, D], reach [n, Hq]): A = sum_j softmax_j |v_j| and reach = the largest |scale|
+    sum_d |q_d k_jd| of a visible key, the sizes an error bound needs."""
+    n, Hq, D = q.shape
+    L, Hkv, _ = k.shape
+    G = Hq // Hkv
+    O, A = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    lse, reach = np.full((n, Hq), -np.inf), np.zeros((n, Hq))
+    for i in range(n):
+        p = L - n + i
+        lo, hi = max(0, p - window + 1) if window else 0, min(p + 1, L)
+        if hi <= lo:
+            continue
+        for h in range(Hq):
+            K, V = k[lo:hi, h // G], v[lo:hi, h // G]
+            s = scale * (K @ q[i, h])
+            m = s.max()
+            e = np.exp(s - m)
+            z = e.sum()
+            O[i, h], A[i, h] = (e / z) @ V, (e / z) @ np.abs(V)
+            lse[i, h] = m + np.log(z)
+            reach[i, h] = abs(scale) * (np.abs(K) @ np.abs(q[i, h])).max()
+    return O, lse, A, reach

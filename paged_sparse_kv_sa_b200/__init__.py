@@ -14,5 +14,7 @@ from ._lib import (EXPORTED, LIB_PATH, SAError, bind, load, page_budget, sa_bloc
                    sa_sparse_step_fp8,
                    sa_select_ambient_heads, sa_sparse_decode_at, sa_sparse_attention_at,
                    sa_build_page_summaries_dir, sa_sparse_step_dir, sa_append_kv_dir,
-                   dir_capacity)
+                   dir_capacity, dense_attention_workspace, sa_append_kv_rope,
+                   sa_append_kv_rope_dir, sa_chunk_attention, sa_chunk_attention_dir,
+                   sa_prompt_attention)
 from .pipeline import SparseDecodeStep, default_splits  # noqa: F401

@@ -19,6 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("PAGED_SPARSE_KV_SA_LIB") or os.path.join(_HERE, "libsa.so")
 
 _c_i64_4 = ctypes.c_int64 * 4
+_c_i64_3 = ctypes.c_int64 * 3
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -79,6 +80,21 @@ _SIGNATURES = {
                                 _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "sa_append_kv_dir": (_I, [_P, _c_i64_4, _P, _c_i64_4, _P, _I, _P, _c_i64_4, _P, _c_i64_4, _P,
                               _I, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "sa_append_kv_rope": (_I, [_P, _c_i64_3, _P, _c_i64_3, _P, _c_i64_3, _P, _I, _P, _I, _I, _I,
+                               _P, _P, _P, _c_i64_4, _P, _c_i64_4, _P, _I, _P, _P, _I, _I, _I, _I,
+                               _I, _I, _P, _P, _P]),
+    "sa_append_kv_rope_dir": (_I, [_P, _c_i64_3, _P, _c_i64_3, _P, _c_i64_3, _P, _I, _P, _I, _I,
+                                   _I, _P, _P, _P, _c_i64_4, _P, _c_i64_4, _P, _I, _P, _I, _I, _P,
+                                   _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "sa_dense_attention_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "sa_chunk_attention": (_I, [_P, _c_i64_3, _P, _I, _P, _c_i64_4, _P, _c_i64_4, _P, _I, _P, _I,
+                                _I, _I, _I, _I, _I, _F, _I, _P, _P, _P, ctypes.c_size_t, _P,
+                                _P]),
+    "sa_chunk_attention_dir": (_I, [_P, _c_i64_3, _P, _I, _P, _c_i64_4, _P, _c_i64_4, _P, _I, _P,
+                                    _I, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P,
+                                    ctypes.c_size_t, _P, _P]),
+    "sa_prompt_attention": (_I, [_P, _c_i64_3, _P, _I, _P, _c_i64_3, _P, _c_i64_3, _P, _I, _I, _I,
+                                 _I, _I, _F, _I, _P, _P, _P, ctypes.c_size_t, _P, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -824,3 +840,247 @@ def sa_append_kv_dir(k_new, v_new, n_new, k_cache, v_cache, page_dir, page_block
            B, Hkv, D, P, P_pool, _ptr(summaries), _ptr(dev_error), _stream(stream)),
           "sa_append_kv_dir")
     return out_seq_lens
+
+
+# ---------------------------------------------------------------------------
+# packed batches: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 of
+# [tokens, heads, D] tensors (cu [B + 1] int32 on the GPU)
+# ---------------------------------------------------------------------------
+def _strides3(t) -> "ctypes.Array":
+    return _c_i64_3(*t.stride())
+
+
+def _on_current(device):
+    """The calls launch on the current device's stream: tensors of another
+    device are refused rather than read from there."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current GPU")
+
+
+def _packed(t, heads, D, device, what):
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise TypeError(f"{what} must be a bfloat16 tensor [tokens, {heads}, {D}]")
+    if t.device != device:
+        raise ValueError("tensors must be on the same GPU")
+    return t
+
+
+def _dense_i32(t, shape, device, what):
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise TypeError(f"{what} must be a contiguous int32 tensor of shape {shape}")
+    if t.device != device:
+        raise ValueError("tensors must be on the same GPU")
+    return t
+
+
+def _dense_out(t, dtype, shape, device, what):
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise TypeError(f"{what} must be a contiguous {dtype} tensor of shape {shape}")
+    if t.device != device:
+        raise ValueError("tensors must be on the same GPU")
+    return t
+
+
+def _cache_pair(k_cache, v_cache, D, device):
+    if (k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 or k_cache.dim() != 4
+            or k_cache.shape != v_cache.shape or k_cache.shape[3] != D):
+        raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
+    if k_cache.device != device or v_cache.device != device:
+        raise ValueError("tensors must be on the same GPU")
+    return k_cache.shape
+
+
+def _error_word(dev_error, device):
+    if dev_error is not None and (dev_error.dtype != torch.int32 or dev_error.device != device):
+        raise TypeError("dev_error must be an int32 tensor on the same GPU")
+    return _ptr(dev_error)
+
+
+def _flat_args(page_table, B, device):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _dense_i32(page_table, (B, page_table.shape[1]), device, "page_table")
+    return _ptr(page_table), page_table.shape[1]
+
+
+def _dir_args_on(page_dir, page_blocks, block_shift, B, device):
+    if page_dir.device != device or page_blocks.device != device:
+        raise ValueError("tensors must be on the same GPU")
+    if page_dir.dim() != 2 or page_dir.shape[0] != B:
+        raise ValueError("page_dir must be [B, n_dir]")
+    return _dir_args(page_dir, page_blocks, block_shift)
+
+
+def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
+    """A workspace for sa_chunk_attention(_dir) and sa_prompt_attention (reusable by
+    calls that do not overlap; large enough for any call of at most total_q tokens)."""
+    n = int(load().sa_dense_attention_workspace_size(total_q, Hq, Hkv, D))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _dense_common(q, cu_q, Hkv, o_out, lse_out, workspace):
+    if q.dim() != 3 or q.dtype != torch.bfloat16:
+        raise TypeError("q must be a bfloat16 tensor [tokens, Hq, D]")
+    dev = q.device
+    _on_current(dev)
+    total, Hq, D = q.shape
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q must be [B + 1]")
+    _dense_i32(cu_q, (cu_q.shape[0],), dev, "cu_q")
+    if o_out is None:
+        o_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _dense_out(o_out, torch.bfloat16, (total, Hq, D), dev, "o_out")
+    if lse_out is None:
+        lse_out = torch.empty((total, Hq), dtype=torch.float32, device=dev)
+    else:
+        _dense_out(lse_out, torch.float32, (total, Hq), dev, "lse_out")
+    if workspace is None:
+        workspace = dense_attention_workspace(total, Hq, Hkv, D, dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise TypeError("workspace must be a contiguous uint8 tensor on the same GPU")
+    return total, Hq, D, cu_q.shape[0] - 1, o_out, lse_out, workspace
+
+
+def _chunk(name, q, k_cache, v_cache, map_args, seq_lens, cu_q, scale, window, o_out, lse_out,
+           workspace, dev_error, stream):
+    lib = load()
+    if k_cache.dim() != 4:
+        raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
+    total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, k_cache.shape[1], o_out,
+                                                               lse_out, workspace)
+    dev = q.device
+    P_pool, Hkv, P, _ = _cache_pair(k_cache, v_cache, D, dev)
+    _dense_i32(seq_lens, (B,), dev, "seq_lens")
+    _call(getattr(lib, name),
+          (_ptr(q), _strides3(q), _ptr(cu_q), total, _ptr(k_cache), _strides4(k_cache),
+           _ptr(v_cache), _strides4(v_cache), *map_args(B, dev), _ptr(seq_lens), B, Hq, Hkv, D, P,
+           P_pool, float(scale), int(window), _ptr(o_out), _ptr(lse_out), _ptr(workspace),
+           workspace.numel(), _error_word(dev_error, dev), _stream(stream)), name)
+    return o_out, lse_out
+
+
+def sa_chunk_attention(q, k_cache, v_cache, page_table, seq_lens, cu_q, scale: float,
+                       window: int = 0, o_out=None, lse_out=None, workspace=None, dev_error=None,
+                       stream=None):
+    """Exact causal attention of packed new tokens q [tokens,Hq,D] (sequence b: tokens
+    cu_q[b] .. cu_q[b + 1] - 1, the last of its seq_lens[b] positions) over the whole paged
+    cache [P_pool,Hkv,P,D]; window > 0 limits a token to its last `window` keys.  workspace:
+    from dense_attention_workspace (a fresh one is made when omitted).  Returns (o
+    [tokens,Hq,D] bf16, lse [tokens,Hq] f32); tokens behind cu_q[B] are left as they were."""
+    return _chunk("sa_chunk_attention", q, k_cache, v_cache,
+                  lambda B, dev: _flat_args(page_table, B, dev), seq_lens, cu_q, scale, window,
+                  o_out, lse_out, workspace, dev_error, stream)
+
+
+def sa_chunk_attention_dir(q, k_cache, v_cache, page_dir, page_blocks, block_shift: int, seq_lens,
+                           cu_q, scale: float, window: int = 0, o_out=None, lse_out=None,
+                           workspace=None, dev_error=None, stream=None):
+    """sa_chunk_attention over a two-level page map."""
+    return _chunk("sa_chunk_attention_dir", q, k_cache, v_cache,
+                  lambda B, dev: _dir_args_on(page_dir, page_blocks, block_shift, B, dev),
+                  seq_lens, cu_q, scale, window, o_out, lse_out, workspace, dev_error, stream)
+
+
+def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_out=None,
+                        lse_out=None, workspace=None, dev_error=None, stream=None):
+    """Exact causal attention over whole packed prompts: q [tokens,Hq,D], k and v
+    [keys,Hkv,D], sequence b at cu_q[b] .. and cu_k[b] .. (normally the same tensor), its
+    queries the last of its key positions.  Returns (o [tokens,Hq,D] bf16, lse)."""
+    lib = load()
+    if k.dim() != 3:
+        raise TypeError("k must be a bfloat16 tensor [keys, Hkv, D]")
+    Hkv = k.shape[1]
+    total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
+                                                               workspace)
+    dev = q.device
+    _packed(k, Hkv, D, dev, "k"), _packed(v, Hkv, D, dev, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must hold the same tokens")
+    _dense_i32(cu_k, (B + 1,), dev, "cu_k")
+    _call(lib.sa_prompt_attention,
+          (_ptr(q), _strides3(q), _ptr(cu_q), total, _ptr(k), _strides3(k), _ptr(v), _strides3(v),
+           _ptr(cu_k), k.shape[0], B, Hq, Hkv, D, float(scale), int(window), _ptr(o_out),
+           _ptr(lse_out), _ptr(workspace), workspace.numel(), _error_word(dev_error, dev),
+           _stream(stream)), "sa_prompt_attention")
+    return o_out, lse_out
+
+
+def _append_rope(name, q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, map_args,
+                 seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream):
+    lib = load()
+    if k_new.dim() != 3 or k_new.dtype != torch.bfloat16:
+        raise TypeError("k_new must be a bfloat16 tensor [tokens, Hkv, D]")
+    dev = k_new.device
+    _on_current(dev)
+    total, Hkv, D = k_new.shape
+    _packed(v_new, Hkv, D, dev, "v_new")
+    if v_new.shape[0] != total:
+        raise ValueError("k_new and v_new must hold the same tokens")
+    if cu_new.dim() != 1 or cu_new.shape[0] < 1:
+        raise ValueError("cu_new must be [B + 1]")
+    B = cu_new.shape[0] - 1
+    _dense_i32(cu_new, (B + 1,), dev, "cu_new")
+    _dense_i32(seq_lens, (B,), dev, "seq_lens")
+    P_pool, heads, P, _ = _cache_pair(k_cache, v_cache, D, dev)
+    if heads != Hkv:
+        raise ValueError("the caches must have k_new's heads")
+    n_pos = rot = 0
+    if rope_table is not None:
+        if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
+                not rope_table.is_contiguous() or rope_table.device != dev:
+            raise TypeError("rope_table must be a contiguous float32 tensor [positions, rot_dim]")
+        n_pos, rot = rope_table.shape
+    Hq = 0
+    qs = _c_i64_3(0, 0, 1)
+    if q_new is not None:
+        if q_new.dim() != 3 or q_new.shape[0] != total:
+            raise ValueError("q_new must hold k_new's tokens")
+        Hq = q_new.shape[1]
+        _packed(q_new, Hq, D, dev, "q_new")
+        qs = _strides3(q_new)
+        if q_out is None:
+            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense_out(q_out, torch.bfloat16, (total, Hq, D), dev, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q_new")
+    if k_out is not None:
+        _dense_out(k_out, torch.bfloat16, (total, Hkv, D), dev, "k_out")
+    if summaries is not None:
+        _dense_out(summaries, torch.bfloat16, (P_pool, Hkv, D), dev, "summaries")
+    if out_seq_lens is not None:
+        _dense_i32(out_seq_lens, (B,), dev, "out_seq_lens")
+    _call(getattr(lib, name),
+          (_ptr(q_new), qs, _ptr(k_new), _strides3(k_new), _ptr(v_new), _strides3(v_new),
+           _ptr(cu_new), total, _ptr(rope_table), n_pos, rot, int(bool(interleaved)), _ptr(q_out),
+           _ptr(k_out), _ptr(k_cache), _strides4(k_cache), _ptr(v_cache), _strides4(v_cache),
+           *map_args(B, dev), _ptr(seq_lens), _ptr(out_seq_lens), B, Hq, Hkv, D, P, P_pool,
+           _ptr(summaries), _error_word(dev_error, dev), _stream(stream)), name)
+    return q_out, out_seq_lens
+
+
+def sa_append_kv_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page_table,
+                      seq_lens, summaries=None, interleaved: bool = False, q_out=None, k_out=None,
+                      out_seq_lens=None, dev_error=None, stream=None):
+    """Append packed tokens (k_new, v_new [tokens,Hkv,D], sequence b: tokens cu_new[b] ..
+    cu_new[b + 1] - 1) at positions seq_lens[b] + i of the paged caches, keys rotated by
+    rope_table [positions, rot_dim] f32 (cosines, then sines; None: no rotation), and
+    rewrite the touched pages' summaries (optional) in place.  q_new [tokens,Hq,D]
+    (optional) is rotated into q_out, the rotated keys also go to k_out when given; both
+    may be the inputs themselves.  Returns (q_out, out_seq_lens)."""
+    return _append_rope("sa_append_kv_rope", q_new, k_new, v_new, cu_new, rope_table, k_cache,
+                        v_cache, lambda B, dev: _flat_args(page_table, B, dev), seq_lens,
+                        summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream)
+
+
+def sa_append_kv_rope_dir(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page_dir,
+                          page_blocks, block_shift: int, seq_lens, summaries=None,
+                          interleaved: bool = False, q_out=None, k_out=None, out_seq_lens=None,
+                          dev_error=None, stream=None):
+    """sa_append_kv_rope over a two-level page map."""
+    return _append_rope("sa_append_kv_rope_dir", q_new, k_new, v_new, cu_new, rope_table, k_cache,
+                        v_cache,
+                        lambda B, dev: _dir_args_on(page_dir, page_blocks, block_shift, B, dev),
+                        seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error,
+                        stream)

@@ -1146,4 +1146,259 @@ int sa_sparse_step_dir(const uint16_t* q, const int64_t q_strides[4], const uint
                    lse_out, workspace, workspace_bytes, dev_error, stream);
 }
 
+namespace {
+// Packed [tokens, heads, D] bf16: 16-byte aligned base, unit feature stride,
+// the others multiples of 8 elements.
+int check_packed(const void* p, const int64_t s[3]) {
+  if (!p || !s) return SA_ERR_INVALID_ARG;
+  if (!aligned16(p) || s[2] != 1) return SA_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    if (s[i] < 0 || (s[i] % 8) != 0) return SA_ERR_INVALID_ARG;
+  return SA_OK;
+}
+// Strides a TMA map takes: positive, below 2^40 bytes.
+bool map_strides(const int64_t* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] <= 0 || s[i] >= (int64_t(1) << 39)) return false;
+  return true;
+}
+
+int rope_append_impl(const uint16_t* q, const int64_t* qs, const uint16_t* k, const int64_t* kn,
+                     const uint16_t* v, const int64_t* vn, const int32_t* cu, int total,
+                     const float* table, int n_pos, int rot, int interleaved, uint16_t* q_out,
+                     uint16_t* k_out, uint16_t* k_cache, const int64_t* ks, uint16_t* v_cache,
+                     const int64_t* vs, const PageMap& pm, int max_pages, const int32_t* seq_lens,
+                     int32_t* out_seq_lens, int B, int Hq, int Hkv, int D, int page_size,
+                     int P_pool, uint16_t* summaries, int32_t* dev_error, void* stream) {
+  if (B < 0 || total < 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || max_pages < 0 ||
+      P_pool <= 0 || n_pos < 0 || rot < 0 || rot > D || D % 8 != 0 || rot % 16 != 0 ||
+      (q && Hq <= 0))
+    return SA_ERR_INVALID_ARG;
+  if (B == 0) return SA_OK;
+  if (!cu || !seq_lens || out_seq_lens == seq_lens) return SA_ERR_INVALID_ARG;
+  if (total > 0) {
+    if (q) {
+      if (int r = check_packed(q, qs)) return r;
+      if (!q_out || !aligned16(q_out)) return SA_ERR_INVALID_ARG;
+    }
+    if (int r = check_packed(k, kn)) return r;
+    if (int r = check_packed(v, vn)) return r;
+  }
+  if (int r = check_cache(k_cache, ks)) return r;
+  if (int r = check_cache(v_cache, vs)) return r;
+  if (!pm.table || (rot > 0 && (!table || !aligned16(table))) || (k_out && !aligned16(k_out)))
+    return SA_ERR_INVALID_ARG;
+  if (D > 256 || (int64_t)max_pages * page_size > 0x7fffffffLL - total) return SA_ERR_UNSUPPORTED;
+  RopeAppendArgs a = {};
+  a.q = q;
+  if (q && qs) a.q0 = qs[0], a.q1 = qs[1];
+  a.k = k;
+  a.v = v;
+  if (total > 0) a.k0 = kn[0], a.k1 = kn[1], a.v0 = vn[0], a.v1 = vn[1];
+  a.cu = cu;
+  a.table = table;
+  a.n_pos = rot > 0 ? n_pos : 0x7fffffffLL;   // without a rotation there is no table to run out of
+  a.rot = rot;
+  a.interleaved = interleaved;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.k_cache = k_cache;
+  a.ks0 = ks[0], a.ks1 = ks[1], a.ks2 = ks[2];
+  a.v_cache = v_cache;
+  a.vs0 = vs[0], a.vs1 = vs[1], a.vs2 = vs[2];
+  a.pt = pm;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.out_seq_lens = out_seq_lens;
+  a.B = B;
+  a.total = total;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.P = page_size;
+  a.P_pool = P_pool;
+  a.sig = summaries;
+  a.err = dev_error;
+  const int64_t ctas = ((int64_t)total / page_size + 2 * (int64_t)B) * Hkv + total;
+  if (ctas > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
+  return cuda_status(launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+// What the dense attention calls share: sizes, outputs, workspace.
+int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int total_q, int B,
+                 int Hq, int Hkv, int D, float scale, int window, uint16_t* o, float* lse,
+                 void* workspace, size_t workspace_bytes, int32_t* dev_error, DenseArgs* a) {
+  if (B < 0 || total_q < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || window < 0 ||
+      !std::isfinite(scale) || !(scale > 0.f))
+    return SA_ERR_INVALID_ARG;
+  if (B == 0 || total_q == 0) return SA_OK;
+  if (int r = check_packed(q, qs)) return r;
+  if (!cu_q || !o || !aligned16(o)) return SA_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > kDenseMaxBatch ||
+      (int64_t)total_q * Hq > 0x7fffffffLL / 2)
+    return SA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < dense_workspace_bytes(total_q, Hq, Hkv, D))
+    return SA_ERR_WORKSPACE;
+  a->q = q;
+  a->q0 = qs[0];
+  a->q1 = qs[1];
+  a->cu_q = cu_q;
+  a->B = B;
+  a->total_q = total_q;
+  a->Hq = Hq;
+  a->Hkv = Hkv;
+  a->D = D;
+  a->window = window < (1 << 30) ? window : 0;   // positions stay below 2^30
+  a->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  a->o = o;
+  a->lse = lse;
+  a->err = dev_error;
+  dense_workspace(a, workspace);
+  return SA_OK;
+}
+
+int chunk_impl(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int total_q,
+               const uint16_t* k_cache, const int64_t* ks, const uint16_t* v_cache,
+               const int64_t* vs, const PageMap& pm, int max_pages, const int32_t* seq_lens,
+               int B, int Hq, int Hkv, int D, int page_size, int P_pool, float scale, int window,
+               uint16_t* o, float* lse, void* workspace, size_t workspace_bytes,
+               int32_t* dev_error, void* stream) {
+  DenseArgs a = {};
+  if (page_size <= 0 || max_pages < 0 || P_pool <= 0) return SA_ERR_INVALID_ARG;
+  if (int r = dense_common(q, qs, cu_q, total_q, B, Hq, Hkv, D, scale, window, o, lse, workspace,
+                           workspace_bytes, dev_error, &a))
+    return r;
+  if (B == 0 || total_q == 0) return SA_OK;
+  if (int r = check_cache(k_cache, ks)) return r;
+  if (int r = check_cache(v_cache, vs)) return r;
+  if (!pm.table || !seq_lens) return SA_ERR_INVALID_ARG;
+  if (page_size % 16 || (int64_t)max_pages * page_size > 0x3fffffffLL || !map_strides(ks, 3) ||
+      !map_strides(vs, 3))
+    return SA_ERR_UNSUPPORTED;
+  a.pt = pm;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.P = page_size;
+  a.P_pool = P_pool;
+  a.box = 16;
+  while (a.box < 128 && page_size % (2 * a.box) == 0) a.box *= 2;
+  CUtensorMap kmap, vmap;
+  if (!encode_kv_map(&kmap, k_cache, D, page_size, Hkv, P_pool, ks, a.box) ||
+      !encode_kv_map(&vmap, v_cache, D, page_size, Hkv, P_pool, vs, a.box))
+    return SA_ERR_CUDA;
+  return cuda_status(launch_dense(a, kmap, vmap, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+int sa_append_kv_rope(const uint16_t* q_new, const int64_t q_strides[3], const uint16_t* k_new,
+                      const int64_t kn_strides[3], const uint16_t* v_new,
+                      const int64_t vn_strides[3], const int32_t* cu_new, int total_new,
+                      const float* rope_table, int n_pos, int rot_dim, int interleaved,
+                      uint16_t* q_out, uint16_t* k_out, uint16_t* k_cache,
+                      const int64_t k_strides[4], uint16_t* v_cache, const int64_t v_strides[4],
+                      const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                      int32_t* out_seq_lens, int B, int Hq, int Hkv, int D, int page_size,
+                      int P_pool, uint16_t* summaries, int32_t* dev_error, void* stream) {
+  return rope_append_impl(q_new, q_strides, k_new, kn_strides, v_new, vn_strides, cu_new,
+                          total_new, rope_table, n_pos, rot_dim, interleaved, q_out, k_out,
+                          k_cache, k_strides, v_cache, v_strides, flat_map(page_table, max_pages),
+                          max_pages, seq_lens, out_seq_lens, B, Hq, Hkv, D, page_size, P_pool,
+                          summaries, dev_error, stream);
+}
+
+int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[3],
+                          const uint16_t* k_new, const int64_t kn_strides[3],
+                          const uint16_t* v_new, const int64_t vn_strides[3],
+                          const int32_t* cu_new, int total_new, const float* rope_table,
+                          int n_pos, int rot_dim, int interleaved, uint16_t* q_out,
+                          uint16_t* k_out, uint16_t* k_cache, const int64_t k_strides[4],
+                          uint16_t* v_cache, const int64_t v_strides[4], const int32_t* page_dir,
+                          int n_dir, const int32_t* page_blocks, int n_blocks, int block_shift,
+                          const int32_t* seq_lens, int32_t* out_seq_lens, int B, int Hq, int Hkv,
+                          int D, int page_size, int P_pool, uint16_t* summaries,
+                          int32_t* dev_error, void* stream) {
+  PageMap m;
+  int max_pages = 0;
+  if (int r = dir_map(page_dir, n_dir, page_blocks, n_blocks, block_shift, &m, &max_pages))
+    return r;
+  return rope_append_impl(q_new, q_strides, k_new, kn_strides, v_new, vn_strides, cu_new,
+                          total_new, rope_table, n_pos, rot_dim, interleaved, q_out, k_out,
+                          k_cache, k_strides, v_cache, v_strides, m, max_pages, seq_lens,
+                          out_seq_lens, B, Hq, Hkv, D, page_size, P_pool, summaries, dev_error,
+                          stream);
+}
+
+size_t sa_dense_attention_workspace_size(int total_q, int Hq, int Hkv, int D) {
+  if (total_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0) return 0;
+  return dense_workspace_bytes(total_q, Hq, Hkv, D);
+}
+
+int sa_chunk_attention(const uint16_t* q, const int64_t q_strides[3], const int32_t* cu_q,
+                       int total_q, const uint16_t* k_cache, const int64_t k_strides[4],
+                       const uint16_t* v_cache, const int64_t v_strides[4],
+                       const int32_t* page_table, int max_pages, const int32_t* seq_lens, int B,
+                       int Hq, int Hkv, int D, int page_size, int P_pool, float scale, int window,
+                       uint16_t* o_out, float* lse_out, void* workspace, size_t workspace_bytes,
+                       int32_t* dev_error, void* stream) {
+  return chunk_impl(q, q_strides, cu_q, total_q, k_cache, k_strides, v_cache, v_strides,
+                    flat_map(page_table, max_pages), max_pages, seq_lens, B, Hq, Hkv, D,
+                    page_size, P_pool, scale, window, o_out, lse_out, workspace, workspace_bytes,
+                    dev_error, stream);
+}
+
+int sa_chunk_attention_dir(const uint16_t* q, const int64_t q_strides[3], const int32_t* cu_q,
+                           int total_q, const uint16_t* k_cache, const int64_t k_strides[4],
+                           const uint16_t* v_cache, const int64_t v_strides[4],
+                           const int32_t* page_dir, int n_dir, const int32_t* page_blocks,
+                           int n_blocks, int block_shift, const int32_t* seq_lens, int B, int Hq,
+                           int Hkv, int D, int page_size, int P_pool, float scale, int window,
+                           uint16_t* o_out, float* lse_out, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  PageMap m;
+  int max_pages = 0;
+  if (int r = dir_map(page_dir, n_dir, page_blocks, n_blocks, block_shift, &m, &max_pages))
+    return r;
+  return chunk_impl(q, q_strides, cu_q, total_q, k_cache, k_strides, v_cache, v_strides, m,
+                    max_pages, seq_lens, B, Hq, Hkv, D, page_size, P_pool, scale, window, o_out,
+                    lse_out, workspace, workspace_bytes, dev_error, stream);
+}
+
+int sa_prompt_attention(const uint16_t* q, const int64_t q_strides[3], const int32_t* cu_q,
+                        int total_q, const uint16_t* k, const int64_t k_strides[3],
+                        const uint16_t* v, const int64_t v_strides[3], const int32_t* cu_k,
+                        int total_k, int B, int Hq, int Hkv, int D, float scale, int window,
+                        uint16_t* o_out, float* lse_out, void* workspace, size_t workspace_bytes,
+                        int32_t* dev_error, void* stream) {
+  DenseArgs a = {};
+  if (total_k < 0) return SA_ERR_INVALID_ARG;
+  if (int r = dense_common(q, q_strides, cu_q, total_q, B, Hq, Hkv, D, scale, window, o_out,
+                           lse_out, workspace, workspace_bytes, dev_error, &a))
+    return r;
+  if (B == 0 || total_q == 0) return SA_OK;
+  if (!cu_k) return SA_ERR_INVALID_ARG;
+  if (total_k > 0) {
+    if (int r = check_packed(k, k_strides)) return r;
+    if (int r = check_packed(v, v_strides)) return r;
+    if (total_k > 0x3fffffff || !map_strides(k_strides, 2) || !map_strides(v_strides, 2))
+      return SA_ERR_UNSUPPORTED;
+  }
+  a.cu_k = cu_k;
+  a.total_k = total_k;
+  a.P = 128;
+  a.P_pool = 1;
+  a.box = 128;
+  // one "page" of total_k rows; without keys nothing is loaded and q stands in
+  const int rows = total_k > 0 ? total_k : 1;
+  const int64_t one[3] = {D, D, 1};
+  const int64_t* ks = total_k > 0 ? k_strides : one;
+  const int64_t* vs = total_k > 0 ? v_strides : one;
+  const int64_t k4[4] = {ks[0], ks[1], ks[0], 1}, v4[4] = {vs[0], vs[1], vs[0], 1};
+  CUtensorMap kmap, vmap;
+  if (!encode_kv_map(&kmap, total_k > 0 ? k : q, D, rows, total_k > 0 ? Hkv : 1, 1, k4, 128) ||
+      !encode_kv_map(&vmap, total_k > 0 ? v : q, D, rows, total_k > 0 ? Hkv : 1, 1, v4, 128))
+    return SA_ERR_CUDA;
+  return cuda_status(launch_dense(a, kmap, vmap, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,816 @@
+// Dense causal attention of packed query tokens on the 5th-generation tensor
+// cores: new tokens over a whole paged cache (single decode tokens, drafts,
+// prompt chunks, mixed in one batch), or whole packed prompts.
+//
+// Query row (token t, head h) of sequence b sits at position L_b - n_b + t and
+// sees the keys j at or before it (and, with a window, j > position - window):
+//   S = scale q.k_j,  O = sum_j softmax(S)_j v_j,  lse = log sum_j exp(S_j).
+// The rows of one (sequence, kv head) are (token, group head) pairs, token
+// major, so a K/V tile is read once for all heads of its group.  An item is 256
+// of these rows; its work is the 128-key tiles any of its rows sees.
+//
+// Work split.  Every CTA (one per SM) takes an equal share of all items' tiles,
+// laid end to end (sequence, kv head, row tile), wherever the share's ends cut
+// an item: long contexts of single tokens, ragged batches and causal triangles
+// all spread evenly.  Every CTA finds its share from the offsets and lengths
+// alone (no plan kernel, no counters).  A cut item's parts go to the workspace
+// (at most one part that starts an item and one that continues an item per CTA)
+// and a second small kernel merges them; whole items are written at once.
+//
+// One CTA, two 128-row tiles A and B:
+//   warps 0-3 / 4-7   softmax of tile A / B, one row per thread: S from TMEM,
+//                 mask (only tiles some row does not see whole), lazily re-based
+//                 base-2 softmax (the running max moves only by more than 2^8,
+//                 so the O rescale through TMEM is rare), P as bf16 over the
+//                 S columns in two 64-key halves, epilogue;
+//   warp 8        issues tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
+//                 with P from TMEM, in the order PV_A(i), QK_A(i+1), PV_B(i),
+//                 QK_B(i+1): one tile's MMAs run under the other's softmax;
+//   warp 9        K and V tiles by TMA through the page map into two rings
+//                 (a missing page loads zeros from an out-of-range coordinate);
+//   warp 10       the next item's queries by cp.async as soon as its buffer frees.
+// An item of at most 128 rows gives both tiles the same rows and every other
+// key tile each ("halves"); the two running softmaxes merge in the epilogue,
+// both accumulators being in the same TMEM lanes.
+//
+// P is one bf16 rounding of each probability (relative 2^-8 at most, the same
+// step as the bf16 output's own rounding); the row sums, and so the LSE, are of
+// the unrounded float32 probabilities.
+#include "common.cuh"
+#include "internal.h"
+#include "tc05.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kPlanWarp = 11;
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;        // keys per tile
+constexpr int kM = 128;           // rows per tile
+constexpr int kMaxSegs = 32;      // segments planned at a time
+constexpr int kItemUnits = 1;     // an item's fixed cost, in tiles
+constexpr int kMinUnits = 2;      // smallest share worth a CTA
+constexpr float kLazy = 8.f;
+constexpr int kBadRing = 8;
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kQBytes = kM * D * 2;
+  static constexpr int kTileBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kDyn = 2 * kQBytes + 2 * kStages * kTileBytes + 1024;
+  static constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kM, kKeys, false, false);
+  static constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kM, D, false, true);
+};
+static_assert(kBadRing > 4 && kDenseRows == 2 * kM, "ring and item shapes");
+
+// ---------------------------------------------------------------- geometry
+struct Seq {
+  int q0, n, k0, L;   // first query token, query tokens, first packed key, keys
+};
+// Offsets and lengths of sequence b, held inside the packed totals and the map
+// (err: also report what was out of range).
+SA_DEV Seq seq_of(const DenseArgs& a, int b, int32_t* err) {
+  Seq s;
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+  s.q0 = min(max(q0, 0), a.total_q);
+  s.n = min(max(q1, s.q0), a.total_q) - s.q0;
+  if (err && (q0 < 0 || q1 < q0 || q1 > a.total_q)) set_dev_error(err, SA_DEVERR_COUNT);
+  if (a.cu_k) {
+    const int k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+    s.k0 = min(max(k0, 0), a.total_k);
+    s.L = min(max(k1, s.k0), a.total_k) - s.k0;
+    if (err && (k0 < 0 || k1 < k0 || k1 > a.total_k)) set_dev_error(err, SA_DEVERR_COUNT);
+  } else {
+    const int L = a.seq_lens[b];
+    s.k0 = 0;
+    s.L = min(max(L, 0), a.max_pages * a.P);
+    if (err && L != s.L) set_dev_error(err, SA_DEVERR_PAGE_RANGE);
+  }
+  return s;
+}
+// Key tiles [x, y) that some row of item qt sees (empty: x == y == 0).
+SA_DEV int2 tiles_of(const Seq& s, int G, int window, int qt) {
+  const int rows = s.n * G, r0 = qt * kDenseRows;
+  const int t_first = r0 / G, t_last = (min(rows, r0 + kDenseRows) - 1) / G;
+  const int hi = min(s.L, s.L - s.n + t_last + 1);
+  const int lo = window ? max(0, s.L - s.n + t_first - window + 1) : 0;
+  if (hi <= lo) return make_int2(0, 0);
+  return make_int2(lo / kKeys, (hi + kKeys - 1) / kKeys);
+}
+SA_DEV int item_units(const Seq& s, int G, int window, int qt) {
+  const int2 t = tiles_of(s, G, window, qt);
+  return kItemUnits + t.y - t.x;
+}
+
+// A run of one item's tiles, as every role needs it.
+struct Seg {
+  int q0, n, k0, L;    // its sequence
+  int b, kvh, r0, nr;  // rows [r0, r0 + nr) of the (sequence, kv head)
+  int j0, j1;          // key tiles of this run
+  int part;            // -1: the whole item, else the workspace part
+  int pad;
+};
+
+// ---------------------------------------------------------------- waits
+SA_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  return false;
+}
+// The same by a whole warp, which goes on together or not at all.
+SA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+// All threads of the CTA, from whichever role's code they are in.
+SA_DEV void cta_sync() { asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory"); }
+// Registers per thread after the roles part: the launch's 384 x 168 divided as
+// 256 x 208 for the softmax warps (a row of scores is 128 registers) + 128 x 88.
+SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+SA_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, n_ctas = gridDim.x;
+  const int G = a.Hq / a.Hkv;
+
+  extern __shared__ uint8_t dyn_smem[];
+  uint8_t* smem = dyn_smem + ((1024 - (smem_u32(dyn_smem) & 1023)) & 1023);
+  uint8_t* q_s = smem;
+  uint8_t* k_s = smem + 2 * C::kQBytes;
+  uint8_t* v_s = k_s + C::kStages * C::kTileBytes;
+  __shared__ uint64_t k_full[C::kStages], k_empty[C::kStages];
+  __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages];
+  __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_s, n_segs_s, last_s;
+  __shared__ Seg seg_s[kMaxSegs];
+  __shared__ uint32_t units_s[kDenseMaxBatch];
+  __shared__ uint32_t bad_s[kBadRing];
+  __shared__ float2 ml_s[2][kM];
+  volatile int* abort_flag = &abort_s;
+
+  // ---- set-up; the units of every sequence (one kv head's) into shared memory
+  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base_s, 512);
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_full[w], 2);
+      mbar_init(&p_full[w][0], 4);
+      mbar_init(&p_full[w][1], 4);
+      mbar_init(&o_done[w], 1);
+    }
+    mbar_init(&q_full, 32);
+    mbar_init(&q_empty, 1);
+    abort_s = 0;
+    fence_mbar_init();
+    a.part_head[cta * 8] = 0;   // no part of this CTA starts an item, so far
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  for (int b = warp; b < a.B; b += kThreads / 32) {
+    const Seq s = seq_of(a, b, cta == 0 && lane == 0 ? a.err : nullptr);
+    const int nqt = (s.n * G + kDenseRows - 1) / kDenseRows;
+    uint32_t u = 0;
+    for (int qt = lane; qt < nqt; qt += 32) u += item_units(s, G, a.window, qt);
+    u = __reduce_add_sync(0xffffffffu, u);
+    if (lane == 0) units_s[b] = u;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base_s;
+
+  uint32_t kc = 0;                  // key tiles so far
+  uint32_t cw[2] = {0, 0};          // S / P hand-overs so far, per tile
+  uint32_t oc[2] = {0, 0};          // accumulators finished so far, per tile
+  uint32_t qc = 0;                  // query loads so far
+  bool ok = true;
+
+  // ---- roles: each runs through the planned segments, a batch at a time
+  if (warp < kSoftWarps) {
+    // ================= softmax and epilogue
+    regs_up();
+    for (bool last = false; !last;) {
+      cta_sync();
+      const int n_segs = n_segs_s;
+      last = last_s;
+      const int w = warp >> 2, quarter = warp & 3;
+      const int row = quarter * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      const uint32_t s_col = tmem + lanes + 128 * w;
+      const uint32_t o_col = tmem + lanes + 256 + D * w;
+      const float sl = a.scale_log2;
+      const int boxes_log2 = 31 - __clz(a.box);
+      for (int i = 0; i < n_segs; ++i) {
+        const Seg s = seg_s[i];
+        const int nt = s.j1 - s.j0;
+        const bool halves = s.nr <= kM;
+        const int n_w = halves ? (w ? nt / 2 : (nt + 1) / 2) : nt;
+        const int n_other = halves ? (w ? (nt + 1) / 2 : nt / 2) : nt;
+        const int rr = (halves ? 0 : w * kM) + row;
+        const bool row_ok = rr < s.nr;
+        const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+        const int rg = s.r0 + rr;
+        const int t = row_ok ? rg / G : 0;
+        const int head = s.kvh * G + (row_ok ? rg - t * G : 0);
+        // visible keys [vis_lo, vis_hi)
+        const int qpos = s.L - s.n + t;
+        const int vis_hi = min(s.L, qpos + 1);
+        const int vis_lo = a.window ? qpos - a.window + 1 : 0;
+        float m_ref = -INFINITY, l = 0.f;
+        for (int it = 0; it < n_w; ++it, ++cw[0]) {
+          const int ti = halves ? 2 * it + w : it;
+          const int k0 = (s.j0 + ti) * kKeys;
+          ok = ok && warp_wait(&s_full[w], cw[0] & 1, abort_flag);
+          if (!ok) break;
+          if (!warp_ok) {   // no rows here: whatever P holds reaches no row that is kept
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&p_full[w][0]);
+              mbar_arrive(&p_full[w][1]);
+            }
+            continue;
+          }
+          tc::fence_after_sync();
+          float x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tc::ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
+          const int lo = vis_lo - k0, hi = vis_hi - k0;
+          const uint32_t bad = bad_s[(kc + ti) % kBadRing];
+          const bool masked =
+              __any_sync(0xffffffffu, bad || (row_ok && (lo > 0 || hi < kKeys)));
+          tc::wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t vis = hi >= 32 * c + 32 ? 0xffffffffu
+                                               : hi > 32 * c ? (1u << (hi - 32 * c)) - 1u : 0u;
+              if (lo > 32 * c)
+                vis &= lo >= 32 * c + 32 ? 0u : ~((1u << (lo - 32 * c)) - 1u);
+              if (bad) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if ((bad >> ((32 * c + 16 * h) >> boxes_log2)) & 1u) vis &= ~(0xffffu << (16 * h));
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((vis >> k) & 1u)) x[32 * c + k] = -INFINITY;
+            }
+          }
+          const float mx = reduce_n<false>(x) * sl;
+          const bool move = mx > m_ref + kLazy;
+          const float m_new = move ? mx : m_ref;
+          const float nb = m_new == -INFINITY ? 0.f : -m_new;
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? exp2f(m_ref - mx) : 1.f;
+            l *= alpha;
+            if (it > 0) {   // this row's PV of the previous tile is complete
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tc::ld32(o_col + c * 32, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tc::st32(o_col + c * 32, o);
+              }
+            }
+          }
+          m_ref = m_new;
+          unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
+          const unsigned long long sl2 = f2_pack(sl, sl), nb2 = f2_pack(nb, nb);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int e = 32 * c + 2 * k;
+              const float2 z = f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), sl2, nb2));
+              const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+              ls[k & 3] = f2_add(ls[k & 3], f2_pack(p0, p1));
+              p[k] = pack_bf16(p0, p1);
+            }
+            tc::st16(s_col + 16 * c, p);
+            if (c & 1) {
+              tc::wait_st();
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[w][c >> 1]);
+            }
+          }
+          const float2 l0 = f2_unpack(f2_add(ls[0], ls[1])), l1 = f2_unpack(f2_add(ls[2], ls[3]));
+          l += (l0.x + l0.y) + (l1.x + l1.y);
+        }
+        // ---- epilogue
+        if (n_w > 0) {
+          ok = ok && warp_wait(&o_done[w], oc[0] & 1, abort_flag);
+          ++oc[0];
+        }
+        float wa = 1.f, wb = 0.f, m_all = m_ref, l_all = l;
+        const int id = 1 + quarter;
+        if (halves) {   // the other half's running max and sum, and its accumulator
+          if (n_other > 0) {
+            ok = ok && warp_wait(&o_done[1 - w], oc[1] & 1, abort_flag);
+            ++oc[1];
+          }
+          ml_s[w][row] = make_float2(m_ref, l);
+          pair_sync(id);
+          const float2 other = ml_s[1 - w][row];
+          m_all = fmaxf(m_ref, other.x);
+          wa = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_all);
+          wb = other.x == -INFINITY ? 0.f : exp2f(other.x - m_all);
+          l_all = l * wa + other.y * wb;
+        } else {
+          if (nt > 0) ++oc[1];
+        }
+        tc::fence_after_sync();
+        const bool empty = !ok || l_all == 0.f;
+        const float inv = empty ? 0.f : 1.f / l_all;
+        wa *= inv;
+        wb *= inv;
+        const bool use_a = n_w > 0, use_b = halves && n_other > 0;
+        const uint32_t b_col = tmem + lanes + 256 + D * (1 - w);
+        const int64_t orow = (int64_t)(s.q0 + t) * a.Hq + head;
+        if (warp_ok) {
+          // halves: each of the two threads of a row writes half of the columns
+          const int c0 = halves ? w * (D / 64) : 0, c1 = halves ? c0 + D / 64 : D / 32;
+          for (int c = c0; c < c1; ++c) {
+            float o[32];
+            if (use_a) {
+              tc::ld32(o_col + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= wa;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            }
+            if (use_b) {
+              float ob[32];
+              tc::ld32(b_col + c * 32, ob);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = fmaf(ob[k], wb, o[k]);
+            }
+            if (empty) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            }
+            if (row_ok) {
+              if (s.part < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(a.o + orow * D + c * 32);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]),
+                                      pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                      pack_bf16(o[8 * k + 4], o[8 * k + 5]),
+                                      pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(
+                    a.part_o + ((int64_t)s.part * a.rows_cap + rr) * D + c * 32);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              }
+            }
+          }
+          if (row_ok && !(halves && w)) {
+            const float lse2 = empty ? -INFINITY : m_all + log2f(l_all);
+            if (s.part >= 0)
+              a.part_lse[(int64_t)s.part * a.rows_cap + rr] = lse2;
+            else if (a.lse)
+              a.lse[orow] = lse2 * kLn2;
+          }
+        }
+        tc::fence_before_sync();
+        if (halves) pair_sync(id);   // both accumulators read: the next item may write them
+        kc += nt;
+      }
+      if (!ok && lane == 0) set_dev_error(a.err, SA_DEVERR_TIMEOUT);
+      cta_sync();
+    }
+  } else {
+    regs_down();
+    if (warp == kLoadWarp) {
+      // ================= K and V tiles
+      for (bool last = false; !last;) {
+        cta_sync();
+        const int n_segs = n_segs_s;
+        last = last_s;
+        const int nb = kKeys / a.box;
+        const int g = lane & (nb - 1), ch = lane / nb;   // box and 64-column chunk of this lane
+        for (int i = 0; i < n_segs && ok; ++i) {
+          const Seg s = seg_s[i];
+          for (int j = s.j0; j < s.j1; ++j, ++kc) {
+            const int st = kc % C::kStages;
+            const uint32_t par = ((kc / C::kStages) - 1) & 1;
+            const int key = j * kKeys + g * a.box;
+            int page = 0, row = s.k0 + key;
+            bool bad = false;
+            if (!a.cu_k) {
+              page = a.P_pool;   // out of range: zeros
+              row = 0;
+              if (key < s.L) {
+                const int ph = page_at(a.pt, s.b, key / a.P);
+                bad = ph < 0 || ph >= a.P_pool;
+                if (!bad) page = ph, row = key % a.P;
+              }
+            }
+            const uint32_t bits = __ballot_sync(0xffffffffu, bad) & ((1u << nb) - 1u);
+            if (kc >= (uint32_t)C::kStages && !warp_wait(&k_empty[st], par, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              bad_s[kc % kBadRing] = bits;
+              if (bits) set_dev_error(a.err, SA_DEVERR_POOL_RANGE);
+              mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
+            }
+            __syncwarp();
+            if (ch < C::kChunks)
+              tma_load_4d(k_s + st * C::kTileBytes + ch * (kKeys * 128) + g * a.box * 128, &kmap,
+                          &k_full[st], ch * 64, row, s.kvh, page);
+            if (kc >= (uint32_t)C::kStages && !warp_wait(&v_empty[st], par, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
+            __syncwarp();
+            if (ch < C::kChunks)
+              tma_load_4d(v_s + st * C::kTileBytes + ch * (kKeys * 128) + g * a.box * 128, &vmap,
+                          &v_full[st], ch * 64, row, s.kvh, page);
+          }
+        }
+        cta_sync();
+      }
+    } else if (warp == kQWarp) {
+      // ================= queries
+      for (bool last = false; !last;) {
+        cta_sync();
+        const int n_segs = n_segs_s;
+        last = last_s;
+        constexpr int kPieces = D / 8, kStep = 32 / kPieces;   // rows per pass of the warp
+        const int pc = lane % kPieces;
+        for (int i = 0; i < n_segs && ok; ++i) {
+          const Seg s = seg_s[i];
+          if (s.j0 == s.j1) continue;
+          if (qc > 0 && !warp_wait(&q_empty, (qc - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          int row = lane / kPieces;
+          int t = (s.r0 + row) / G, h = (s.r0 + row) % G;
+          const uint16_t* base = a.q + s.q0 * a.q0 + (int64_t)s.kvh * G * a.q1 + pc * 8;
+          for (; row < s.nr; row += kStep) {
+            const int r = row & (kM - 1);
+            const uint32_t dst = smem_u32(q_s) + (row / kM) * C::kQBytes + (pc >> 3) * (kM * 128) +
+                                 r * 128 + (((pc & 7) ^ (r & 7)) << 4);
+            cp_async16(dst, base + t * a.q0 + h * a.q1, 16);
+            for (h += kStep; h >= G; h -= G) ++t;
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          tc::fence_proxy_async();
+          mbar_arrive(&q_full);
+          ++qc;
+        }
+        cta_sync();
+      }
+    } else if (warp == kMmaWarp) {
+      // ================= MMA issue
+      for (bool last = false; !last;) {
+        cta_sync();
+        const int n_segs = n_segs_s;
+        last = last_s;
+        const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(k_s), v_addr = smem_u32(v_s);
+        for (int i = 0; i < n_segs && ok; ++i) {
+          const Seg s = seg_s[i];
+          const int nt = s.j1 - s.j0;
+          if (nt == 0) continue;
+          const bool halves = s.nr <= kM;
+          const int n_w[2] = {halves ? (nt + 1) / 2 : nt, halves ? nt / 2 : nt};
+          int qk_left = n_w[0] + n_w[1];
+          const int t_last = (s.r0 + s.nr - 1) / G;
+          const int hi = min(s.L, s.L - s.n + t_last + 1);
+          auto tile = [&](int it, int w) { return halves ? 2 * it + w : it; };
+          auto qk = [&](int it, int w) {
+            const uint32_t c = kc + tile(it, w);
+            const int st = c % C::kStages;
+            if (halves || w == 0) {
+              if (!warp_wait(&k_full[st], (c / C::kStages) & 1, abort_flag)) return false;
+              tc::fence_after_sync();
+            }
+            if (lane == 0) {
+              const uint32_t qb = q_addr + (halves ? 0 : w) * C::kQBytes;
+              const uint32_t kb = k_addr + st * C::kTileBytes;
+  #pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = (kk >> 2) * (kM * 128) + (kk & 3) * 32;
+                tc::mma_bf16(tmem + 128 * w, tc::sdesc_sw128(qb + o, 16, 1024),
+                             tc::sdesc_sw128(kb + o, 16, 1024), C::kIdQK, kk > 0 ? 1u : 0u);
+              }
+              tc::commit(&s_full[w]);
+              mbar_arrive(&s_full[w]);   // releases bad_s to the softmax warps
+              if (halves || w == 1) tc::commit(&k_empty[st]);
+              if (qk_left == 1) tc::commit(&q_empty);
+            }
+            --qk_left;
+            return true;
+          };
+          auto pv = [&](int it, int w) {
+            const uint32_t c = kc + tile(it, w);
+            const int st = c % C::kStages, j = s.j0 + tile(it, w);
+            // 16-key steps some row of the item sees
+            const int steps = min(8, (hi - j * kKeys + 15) / 16);
+            for (int h = 0; h < 2; ++h) {
+              if (!warp_wait(&p_full[w][h], cw[w] & 1, abort_flag)) return false;
+              if (h == 0 && (halves || w == 0)) {
+                if (!warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag)) return false;
+                // value rows past the sequence's end may hold anything: 0 * NaN
+                const int z0 = max(0, s.L - j * kKeys), nz = 16 * steps - z0;
+                if (nz > 0) {
+                  uint8_t* vt = v_s + st * C::kTileBytes;
+                  for (int x = lane; x < nz * C::kChunks * 8; x += 32) {
+                    const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
+                    *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 +
+                                              (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+                  }
+                  tc::fence_proxy_async();
+                  __syncwarp();
+                }
+              }
+              tc::fence_after_sync();
+              if (lane == 0) {
+                const uint32_t vb = v_addr + st * C::kTileBytes;
+  #pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                  const int kk = 4 * h + k4;
+                  if (kk < steps)
+                    tc::mma_bf16_ts(tmem + 256 + D * w, tmem + 128 * w + 8 * kk,
+                                    tc::sdesc_sw128(vb + kk * 2048, kKeys * 128, 1024), C::kIdPV,
+                                    (it > 0 || kk > 0) ? 1u : 0u);
+                }
+              }
+            }
+            ++cw[w];
+            if (lane == 0 && (halves || w == 1)) tc::commit(&v_empty[st]);
+            return true;
+          };
+          ok = warp_wait(&q_full, qc & 1, abort_flag);
+          tc::fence_after_sync();
+          ok = ok && qk(0, 0) && (n_w[1] == 0 || qk(0, 1));
+          for (int it = 0; ok && it < n_w[0]; ++it) {
+  #pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (!ok || it >= n_w[w]) continue;
+              ok = pv(it, w);
+              if (!ok) continue;
+              if (it + 1 < n_w[w])
+                ok = qk(it + 1, w);
+              else if (lane == 0)
+                tc::commit(&o_done[w]);
+            }
+          }
+          kc += nt;
+          ++qc;
+        }
+        cta_sync();
+      }
+    } else if (warp == kPlanWarp) {
+      // ================= planner
+      // ---- this CTA's share [w_lo, w_hi) of all units, and where it starts
+      int64_t w_total = 0, w_pos = 0, w_hi = 0;   // w_pos: the next unit to plan
+      int n_eff = 1, cb = 0, ckvh = 0, cqt = 0;   // the item that holds w_pos
+      int64_t c_off = 0;                          // units of that item before w_pos
+        int64_t part = 0;
+        for (int b = lane; b < a.B; b += 32) part += units_s[b];
+        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        w_total = part * a.Hkv;
+        n_eff = (int)min((int64_t)n_ctas, max((int64_t)1, w_total / kMinUnits));
+        if (cta < n_eff) {
+          w_pos = w_total * cta / n_eff;
+          w_hi = w_total * (cta + 1) / n_eff;
+        }
+        if (w_pos < w_hi) {
+          // the sequence: 32 at a time
+          int64_t before = 0;
+          for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + lane;
+            int64_t incl = b < a.B ? units_s[b] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += y;
+            }
+            const uint32_t m =
+                __ballot_sync(0xffffffffu, b < a.B && (before + incl) * a.Hkv > w_pos);
+            if (m) {
+              const int src = __ffs(m) - 1;
+              cb = b0 + src;
+              const int64_t i = __shfl_sync(0xffffffffu, incl, src);
+              before += i - units_s[cb];
+              break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+          }
+          int64_t off = w_pos - before * a.Hkv;
+          ckvh = (int)(off / units_s[cb]);
+          off -= (int64_t)ckvh * units_s[cb];
+          // the row tile: 32 at a time
+          const Seq s = seq_of(a, cb, nullptr);
+          const int nqt = (s.n * G + kDenseRows - 1) / kDenseRows;
+          for (int q0 = 0; q0 < nqt; q0 += 32) {
+            const int qt = q0 + lane;
+            int incl = qt < nqt ? item_units(s, G, a.window, qt) : 0;
+            const int own = incl;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += y;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, qt < nqt && incl > off);
+            if (m) {
+              const int src = __ffs(m) - 1;
+              cqt = q0 + src;
+              c_off = off - __shfl_sync(0xffffffffu, incl - own, src);
+              break;
+            }
+            off -= __shfl_sync(0xffffffffu, incl, 31);
+          }
+        }
+      do {
+        // the next segments
+        if (lane == 0) {
+          int ns = 0;
+          while (w_pos < w_hi && ns < kMaxSegs && cb < a.B) {
+            const Seq s = seq_of(a, cb, nullptr);
+            const int rows = s.n * G;
+            const int nqt = (rows + kDenseRows - 1) / kDenseRows;
+            while (w_pos < w_hi && ns < kMaxSegs && ckvh < a.Hkv && nqt > 0) {
+              const int2 t = tiles_of(s, G, a.window, cqt);
+              const int nt = t.y - t.x, units = kItemUnits + nt;
+              const int ua = (int)c_off;
+              const int ub = (int)min((int64_t)units, c_off + (w_hi - w_pos));
+              // units past the item's fixed cost are its tiles
+              const int ta = max(0, ua - kItemUnits), tb = max(0, ub - kItemUnits);
+              if (tb > ta || nt == 0) {
+                Seg& g = seg_s[ns++];
+                g.q0 = s.q0, g.n = s.n, g.k0 = s.k0, g.L = s.L;
+                g.b = cb, g.kvh = ckvh;
+                g.r0 = cqt * kDenseRows;
+                g.nr = min(kDenseRows, rows - g.r0);
+                g.j0 = t.x + ta, g.j1 = t.x + tb;
+                g.part = -1;
+                if (ta > 0 || tb < nt) {
+                  g.part = 2 * cta + (ta == 0);
+                  if (ta == 0) {   // the parts that follow are the next CTAs' first ones
+                    const int64_t e = w_pos - ua + units;   // the item's end
+                    const int last = (int)((e * n_eff + w_total - 1) / w_total) - 1;
+                    int32_t* h = a.part_head + cta * 8;
+                    h[0] = g.nr, h[1] = last - cta + 1;
+                    h[2] = s.q0, h[3] = g.r0, h[4] = ckvh;
+                  }
+                }
+              }
+              w_pos += ub - ua;
+              c_off = 0;
+              if (ub == units && ++cqt == nqt) cqt = 0, ++ckvh;
+            }
+            if (ckvh == a.Hkv || nqt == 0) ckvh = 0, cqt = 0, ++cb;
+          }
+          n_segs_s = ns;
+          last_s = w_pos >= w_hi || cb >= a.B;
+        }
+        cta_sync();
+        cta_sync();
+      } while (!last_s);
+    }
+  }
+  if (warp == kLoadWarp && abort_s) {
+    // give up only when no copy of this CTA is in flight any more
+    for (uint32_t c = kc > (uint32_t)C::kStages ? kc - C::kStages : 0; c <= kc; ++c) {
+      mbar_wait_bounded(&k_full[c % C::kStages], (c / C::kStages) & 1);
+      if (c < kc) mbar_wait_bounded(&v_full[c % C::kStages], (c / C::kStages) & 1);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the cut items: block x takes the item that starts in CTA x's share.
+// One warp per row, four columns per lane; part 0 is CTA x's starting part, the
+// others the continuing parts of the CTAs after it.
+template <int D>
+__global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
+  const int32_t* h = a.part_head + blockIdx.x * 8;
+  const int nr = h[0];
+  if (nr == 0) return;
+  const int np = h[1], q0 = h[2], r0 = h[3], kvh = h[4];
+  const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = blockIdx.x;
+  auto part = [&](int p) { return p == 0 ? 2 * x + 1 : 2 * (x + p); };
+  for (int rr = blockIdx.y * 8 + warp; rr < nr; rr += gridDim.y * 8) {
+    float m = -INFINITY;
+    for (int p = lane; p < np; p += 32)
+      m = fmaxf(m, a.part_lse[(int64_t)part(p) * a.rows_cap + rr]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float tot = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < np && m != -INFINITY; p0 += 32) {
+      const int p = p0 + lane;
+      const float wl =
+          p < np ? exp2f(a.part_lse[(int64_t)part(p) * a.rows_cap + rr] - m) : 0.f;
+      tot += wl;
+      const int cnt = min(32, np - p0);
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wl, i);
+        if (lane < D / 4) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              a.part_o + ((int64_t)part(p0 + i) * a.rows_cap + rr) * D + lane * 4);
+          acc.x = fmaf(wi, v.x, acc.x);
+          acc.y = fmaf(wi, v.y, acc.y);
+          acc.z = fmaf(wi, v.z, acc.z);
+          acc.w = fmaf(wi, v.w, acc.w);
+        }
+      }
+    }
+    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    const float inv = m == -INFINITY ? 0.f : 1.f / tot;
+    const int rg = r0 + rr, t = rg / G;
+    const int64_t orow = (int64_t)(q0 + t) * a.Hq + kvh * G + (rg - t * G);
+    if (lane < D / 4)
+      *reinterpret_cast<uint2*>(a.o + orow * D + lane * 4) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (lane == 0 && a.lse) a.lse[orow] = m == -INFINITY ? m : (m + log2f(tot)) * kLn2;
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  e = allow_max_dyn_smem(reinterpret_cast<const void*>(dense_kernel<D>));
+  if (e != cudaSuccess) return e;
+  const int ctas = sms < kDenseMaxCtas ? sms : kDenseMaxCtas;
+  dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, kmap, vmap);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int by = (a.rows_cap + 31) / 32;   // 32 rows per block
+  dense_merge_kernel<D><<<dim3(ctas, by), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+int rows_cap_of(int total_q, int Hq, int Hkv) {
+  const int64_t rows = (int64_t)total_q * (Hq / Hkv);
+  return (int)(rows < kDenseRows ? rows : kDenseRows);
+}
+size_t r16(size_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+size_t dense_workspace_bytes(int total_q, int Hq, int Hkv, int D) {
+  const size_t rows = 2 * (size_t)kDenseMaxCtas * rows_cap_of(total_q, Hq, Hkv);
+  return kDenseMaxCtas * 32 + r16(rows * 4) + rows * D * 4;
+}
+void dense_workspace(DenseArgs* a, void* ws) {
+  a->rows_cap = rows_cap_of(a->total_q, a->Hq, a->Hkv);
+  const size_t rows = 2 * (size_t)kDenseMaxCtas * a->rows_cap;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  a->part_head = reinterpret_cast<int32_t*>(p);
+  a->part_lse = reinterpret_cast<float*>(p + kDenseMaxCtas * 32);
+  a->part_o = reinterpret_cast<float*>(p + kDenseMaxCtas * 32 + r16(rows * 4));
+}
+
+cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         cudaStream_t stream) {
+  switch (a.D) {
+    case 64: return launch_d<64>(a, kmap, vmap, stream);
+    case 128: return launch_d<128>(a, kmap, vmap, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace sa

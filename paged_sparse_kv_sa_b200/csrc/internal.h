@@ -247,6 +247,69 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 
+// Dense attention of packed query tokens (sequence b: tokens cu_q[b] ..
+// cu_q[b + 1] - 1, the last of its L_b positions) over paged or packed keys.
+struct DenseArgs {
+  const uint16_t* q;       // [total_q, Hq, D]
+  int64_t q0, q1;
+  const int32_t* cu_q;     // [B + 1]
+  const int32_t* cu_k;     // [B + 1] offsets of packed keys (null: paged keys)
+  int total_k;             // packed keys in all
+  PageMap pt;              // paged keys
+  int max_pages;
+  const int32_t* seq_lens; // [B] (paged)
+  int B, total_q, Hq, Hkv, D, P, P_pool;
+  int box;                 // rows of a K / V load: divides the page size and 128
+  int window;              // 0: every earlier key
+  float scale_log2;
+  uint16_t* o;             // [total_q, Hq, D]
+  float* lse;              // [total_q, Hq] (optional)
+  // workspace: the parts of items cut between CTAs
+  int rows_cap;            // rows one part may hold
+  int32_t* part_head;      // [kDenseMaxCtas][8]
+  float* part_lse;         // [2 * kDenseMaxCtas][rows_cap], base 2
+  float* part_o;           // [2 * kDenseMaxCtas][rows_cap][D]
+  int32_t* err;
+};
+constexpr int kDenseMaxCtas = 160;    // persistent CTAs of a launch, at most
+constexpr int kDenseMaxBatch = 4096;  // sequences
+constexpr int kDenseRows = 256;       // query rows (tokens x heads of a group) of an item
+size_t dense_workspace_bytes(int total_q, int Hq, int Hkv, int D);
+// Point the workspace fields of `a` into `ws`.
+void dense_workspace(DenseArgs* a, void* ws);
+cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         cudaStream_t stream);
+
+// Packed new tokens (sequence b: tokens cu[b] .. cu[b + 1] - 1) rotated into
+// the paged cache, and the queries with them.
+struct RopeAppendArgs {
+  const uint16_t* q;       // [total, Hq, D] (null: no queries)
+  int64_t q0, q1;
+  const uint16_t* k;       // [total, Hkv, D]
+  int64_t k0, k1;
+  const uint16_t* v;       // [total, Hkv, D]
+  int64_t v0, v1;
+  const int32_t* cu;       // [B + 1]
+  const float* table;      // [n_pos, rot]: cosines, then sines
+  int64_t n_pos;
+  int rot, interleaved;
+  uint16_t* q_out;         // [total, Hq, D] contiguous
+  uint16_t* k_out;         // [total, Hkv, D] contiguous (optional)
+  uint16_t* k_cache;
+  int64_t ks0, ks1, ks2;
+  uint16_t* v_cache;
+  int64_t vs0, vs1, vs2;
+  PageMap pt;
+  int max_pages;
+  const int32_t* seq_lens;
+  int32_t* out_seq_lens;
+  int B, total, Hq, Hkv, D, P, P_pool;
+  uint16_t* sig;           // [P_pool, Hkv, D] (optional)
+  int32_t* err;
+  int page_ctas;           // set by the launcher
+};
+cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream);
+
 cudaError_t launch_block_union(const float* scores, int Hq, int Hkv, int NQB, int NKB, int q_off,
                                int top_k, int n_sink, int32_t* tables, int32_t* counts,
                                cudaStream_t stream);

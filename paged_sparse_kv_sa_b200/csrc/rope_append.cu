@@ -1,0 +1,283 @@
+// Appending packed new tokens to the paged cache with the rotary position
+// rotation applied on the way: keys are rotated as they are written into their
+// pages, values copied, the queries rotated in the same launch, and the key
+// summaries of the pages that grow recomputed from the stored (rotated,
+// rounded) keys, so that the page router, the sparse step and the dense
+// attention all see one cache.
+//
+// Rotation of one head row x at position p with c = table[p, k], s =
+// table[p, r/2 + k] (k < r/2): (x_i, x_j) -> (x_i c - x_j s, x_j c + x_i s) with
+// (i, j) = (k, k + r/2), or (2k, 2k + 1) when interleaved; features past r are
+// copied.  Every product and sum is one float32 rounding (no contraction), the
+// result one rounding to bf16: the stored bits are those of the plain formula.
+//
+// Two kinds of CTA share the launch.  A page CTA owns one (touched page, kv
+// head): its threads own fixed columns (16-byte pieces, both halves of a
+// rotated pair) and stride over the page's rows, so each reads the old keys or
+// the new ones, rotates, writes, and sums its columns in float64 on the way;
+// the row groups' sums meet in shared memory.  A query CTA rotates the heads of
+// a few tokens.  Page slots and tokens find their sequence by a 32-way search
+// of the offsets: slot s belongs to the last b with floor(cu[b]/P) + 2b <= s
+// (n tokens touch at most floor(n/P) + 2 pages), so the grid needs only the
+// packed total.  Memory-bound: every byte is moved once.
+//
+// Sources: "Universal Attention Engine — Declarative Sparse Attention for
+// Production", "Architecture" (a PagedAttention-compatible cache) and
+// "Content-Dependent Dynamic Routing" (the router scores mean(k_blocks)); the
+// rotation is RoFormer's (Su et al., 2021).
+#include "common.cuh"
+#include "exact.cuh"
+#include "internal.h"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxCols = 256;   // D
+constexpr int kQTokens = 8;     // tokens per query CTA (one per warp)
+
+// Last b in [0, B) with key(b) <= x (key ascending, key(0) <= x); whole warp.
+template <typename F>
+SA_DEV int last_le(int B, int64_t x, F&& key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = B;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int off = lane * step;
+    const bool le = off < len && key(lo + off) <= x;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int idx = m ? 31 - __clz(m) : 0;
+    lo += idx * step;
+    len = min(step, len - idx * step);
+  }
+  return lo;
+}
+
+SA_DEV float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+SA_DEV float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+struct Pieces {   // one unit: 8 columns, or 8 + their 8 partners
+  uint4 a, b;
+};
+
+// Rotate 8 pairs (a_k, b_k) of 16-bit pieces by c, s.
+SA_DEV void rotate_halves(Pieces& u, const float* __restrict__ cs, int r2, int k0) {
+  uint32_t* pa = reinterpret_cast<uint32_t*>(&u.a);
+  uint32_t* pb = reinterpret_cast<uint32_t*>(&u.b);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k0 + 4 * q));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + r2 + k0 + 4 * q));
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t wa = pa[2 * q + i], wb = pb[2 * q + i];
+      const float a0 = bf_lo(wa), a1 = bf_hi(wa), b0 = bf_lo(wb), b1 = bf_hi(wb);
+      const float c0 = cc[2 * i], c1 = cc[2 * i + 1], s0 = ss[2 * i], s1 = ss[2 * i + 1];
+      pa[2 * q + i] = pack_bf16(__fsub_rn(__fmul_rn(a0, c0), __fmul_rn(b0, s0)),
+                                __fsub_rn(__fmul_rn(a1, c1), __fmul_rn(b1, s1)));
+      pb[2 * q + i] = pack_bf16(__fadd_rn(__fmul_rn(b0, c0), __fmul_rn(a0, s0)),
+                                __fadd_rn(__fmul_rn(b1, c1), __fmul_rn(a1, s1)));
+    }
+  }
+}
+// Rotate the 4 adjacent pairs of one piece.
+SA_DEV void rotate_pairs(uint4& x, const float* __restrict__ cs, int r2, int k0) {
+  const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k0));
+  const float4 s = __ldg(reinterpret_cast<const float4*>(cs + r2 + k0));
+  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+  uint32_t* p = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = bf_lo(p[i]), b = bf_hi(p[i]);
+    p[i] = pack_bf16(__fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i])),
+                     __fadd_rn(__fmul_rn(b, cc[i]), __fmul_rn(a, ss[i])));
+  }
+}
+
+// Column of unit u's first piece, and of its second (-1: none).  Halves: units
+// [0, r/16) pair columns 8u and 8u + r/2, the rest copy one piece.
+SA_DEV int2 unit_cols(int u, int r, bool inter) {
+  if (inter) return make_int2(8 * u, -1);
+  const int np = r / 16;
+  return u < np ? make_int2(8 * u, 8 * u + r / 2) : make_int2(r + 8 * (u - np), -1);
+}
+SA_DEV Pieces load_unit(const uint16_t* row, int2 c) {
+  Pieces p;
+  p.a = *reinterpret_cast<const uint4*>(row + c.x);
+  p.b = c.y >= 0 ? *reinterpret_cast<const uint4*>(row + c.y) : make_uint4(0, 0, 0, 0);
+  return p;
+}
+SA_DEV void store_unit(uint16_t* row, int2 c, const Pieces& p) {
+  *reinterpret_cast<uint4*>(row + c.x) = p.a;
+  if (c.y >= 0) *reinterpret_cast<uint4*>(row + c.y) = p.b;
+}
+SA_DEV void rotate_unit(Pieces& p, int2 c, const float* cs, int r, bool inter) {
+  if (c.y >= 0)
+    rotate_halves(p, cs, r / 2, c.x);
+  else if (inter && c.x < r)
+    rotate_pairs(p.a, cs, r / 2, c.x / 2);
+}
+
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendArgs a) {
+  pdl_wait_and_release();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int D = a.D, r = a.rot;
+  const bool inter = a.interleaved != 0;
+  const int upr = inter ? D / 8 : r / 16 + (D - r) / 8;   // units per row
+  if (blockIdx.x >= a.page_ctas) {
+    // ================= queries: one token per warp
+    const int t = (blockIdx.x - a.page_ctas) * kQTokens + (tid >> 5);
+    if (t >= a.total) return;
+    const int b = last_le(a.B, t, [&](int i) { return (int64_t)a.cu[i]; });
+    const int64_t i = (int64_t)t - a.cu[b];
+    const int L = a.seq_lens[b];
+    if (i < 0 || t >= a.cu[b + 1] || L < 0) return;   // behind the last sequence
+    const int64_t pos = L + i;
+    if (pos >= a.n_pos) {
+      if (lane == 0) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
+      return;
+    }
+    const float* cs = a.table + pos * r;
+    for (int x = lane; x < a.Hq * upr; x += 32) {
+      const int h = x / upr, u = x - h * upr;
+      const int2 c = unit_cols(u, r, inter);
+      Pieces p = load_unit(a.q + t * a.q0 + h * a.q1, c);
+      rotate_unit(p, c, cs, r, inter);
+      store_unit(a.q_out + ((int64_t)t * a.Hq + h) * D, c, p);
+    }
+    return;
+  }
+  // ================= one touched page of one kv head
+  __shared__ double sum_s[kThreads * 16];       // [row group][column]
+  __shared__ uint16_t exp_s[kThreads * 16];     // largest << 8 | smallest exponent field
+  const int h = blockIdx.x % a.Hkv, s = blockIdx.x / a.Hkv;
+  const int P = a.P;
+  const int b = last_le(a.B, s, [&](int i) { return (int64_t)(a.cu[i] / P) + 2 * i; });
+  const bool lead = tid == 0 && h == 0;
+  const int t0 = a.cu[b], t1 = a.cu[b + 1], L = a.seq_lens[b];
+  const int j = s - (t0 / P + 2 * b);
+  if (t0 < 0 || t1 < t0 || t1 > a.total) {
+    if (lead) set_dev_error(a.err, SA_DEVERR_COUNT);
+    return;
+  }
+  const int64_t cap = (int64_t)a.max_pages * P;
+  if (L < 0 || L > cap) {
+    if (lead) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
+    return;
+  }
+  const int n = t1 - t0;
+  if (j == 0 && lead && a.out_seq_lens) a.out_seq_lens[b] = L + n;
+  int64_t end = (int64_t)L + n;
+  if (end > cap || end > a.n_pos) {   // tokens past the page map or the table are dropped
+    if (lead && j == 0 && n > 0) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
+    end = cap < a.n_pos ? cap : a.n_pos;
+  }
+  const int64_t p = L / P + j, p0 = p * P;
+  if (j < 0 || end <= L || p0 >= end) return;
+  const int ph = page_at(a.pt, b, (int)p);
+  if (ph < 0 || ph >= a.P_pool) {
+    if (tid == 0) set_dev_error(a.err, SA_DEVERR_POOL_RANGE);
+    return;
+  }
+  const int n_old = (int)(L > p0 ? L - p0 : 0);
+  const int nval = (int)((end < p0 + P ? end : p0 + P) - p0);
+  const int64_t tok0 = t0 + p0 - L;               // token of row 0 (rows >= n_old are new)
+  uint16_t* kpage = a.k_cache + ph * a.ks0 + h * a.ks1;
+  uint16_t* vpage = a.v_cache + ph * a.vs0 + h * a.vs1;
+  // ---- values: copied
+  const int cpr = D / 8;
+  for (int x = tid; x < (nval - n_old) * cpr; x += kThreads) {
+    const int row = n_old + x / cpr, c = (x % cpr) * 8;
+    *reinterpret_cast<uint4*>(vpage + row * a.vs2 + c) =
+        *reinterpret_cast<const uint4*>(a.v + (tok0 + row) * a.v0 + h * a.v1 + c);
+  }
+  // ---- keys: rotated, stored and summed (old rows only summed)
+  const int groups = kThreads / upr;              // row groups; upr <= 32
+  const int g = tid / upr, u = tid - g * upr;
+  const int2 c = unit_cols(u, r, inter);
+  const int ncol = c.y >= 0 ? 16 : 8;
+  double acc[16];
+  int emax[16], emin[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.0, emax[k] = 0, emin[k] = 255;
+  if (g < groups) {
+    for (int row = a.sig ? g : n_old + g; row < nval; row += groups) {
+      Pieces x;
+      if (row < n_old) {
+        x = load_unit(kpage + row * a.ks2, c);
+      } else {
+        x = load_unit(a.k + (tok0 + row) * a.k0 + h * a.k1, c);
+        rotate_unit(x, c, a.table + (p0 + row) * r, r, inter);
+        store_unit(kpage + row * a.ks2, c, x);
+        if (a.k_out) store_unit(a.k_out + ((tok0 + row) * a.Hkv + h) * D, c, x);
+      }
+      if (a.sig) {
+        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t bits = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+          const int e = max(1, (int)((bits >> 7) & 0xffu));   // zeros: skipped below
+          if (bits & 0x7fffu) {
+            emax[k] = max(emax[k], e);
+            emin[k] = min(emin[k], e);
+          }
+          acc[k] += static_cast<double>(bf16_bits_to_float(bits));
+        }
+      }
+    }
+  }
+  if (!a.sig) return;
+  if (g < groups) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k >= ncol) continue;
+      const int d = k < 8 ? c.x + k : c.y + k - 8;
+      sum_s[g * D + d] = acc[k];
+      exp_s[g * D + d] = static_cast<uint16_t>(emax[k] << 8 | emin[k]);
+    }
+  }
+  __syncthreads();
+  const int lg = 32 - __clz(nval);   // >= ceil(log2 nval) + 1
+  for (int d = tid; d < D; d += kThreads) {
+    double t = 0.0;
+    int hi = 0, lo = 255;
+    for (int q = 0; q < min(groups, nval); ++q) {
+      t += sum_s[q * D + d];
+      hi = max(hi, exp_s[q * D + d] >> 8);
+      lo = min(lo, exp_s[q * D + d] & 0xff);
+    }
+    // |x| < 2^(hi - 126) and a multiple of 2^(lo - 134): the float64 sum is
+    // exact in any order while that span and the carries fit 53 bits
+    if (hi > 0 && hi - lo + 8 + lg > 53) {
+      ExactAcc e;
+      e.clear();
+      for (int row = 0; row < nval; ++row) {   // this block's own stores: visible after the barrier
+        uint32_t m;
+        int ex;
+        bool neg;
+        bf16_fields(*(volatile uint16_t*)(kpage + row * a.ks2 + d), m, ex, neg);
+        e.add(m, ex, neg);
+      }
+      t = e.round_to_double();
+    }
+    a.sig[((int64_t)ph * a.Hkv + h) * D + d] = f64_to_bf16_rne(t / static_cast<double>(nval));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream) {
+  if (a.B == 0) return cudaSuccess;
+  static_assert(kMaxCols / 8 <= 32, "a row's units fit one row group");
+  // (page, kv head) CTAs first: their chains (search, table, page, sums) are the longest
+  const int64_t pages = (int64_t)a.total / a.P + 2 * (int64_t)a.B;
+  const int64_t page_ctas = pages * a.Hkv;
+  const int64_t q_ctas = a.q ? (a.total + kQTokens - 1) / kQTokens : 0;
+  if (page_ctas + q_ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  a.page_ctas = (int)page_ctas;
+  return launch_pdl(rope_append_kernel, dim3((unsigned)(page_ctas + q_ctas)), dim3(kThreads), 0,
+                    stream, a);
+}
+
+}  // namespace sa
