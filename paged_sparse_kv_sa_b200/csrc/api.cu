@@ -226,6 +226,21 @@ bool encode_kv_map(CUtensorMap* map, const void* base, int D, int P, int Hkv, in
   return r == CUDA_SUCCESS;
 }
 
+bool encode_q_map(CUtensorMap* map, const void* base, int D, int Hq, int total, int64_t tok_stride,
+                  int64_t head_stride, int G, int toks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)total, 1};
+  cuuint64_t gstr[3] = {(cuuint64_t)head_stride * 2, (cuuint64_t)tok_stride * 2,
+                        (cuuint64_t)tok_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)toks, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, gstr,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_kv_map_u8(CUtensorMap* map, const void* base, int D, int P, int Hkv, int P_pool,
                       const int64_t strides[4]) {
   auto fn = encode_fn();
@@ -1235,7 +1250,7 @@ int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int 
   if (int r = check_packed(q, qs)) return r;
   if (!cu_q || !o || !aligned16(o)) return SA_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > kDenseMaxBatch ||
-      (int64_t)total_q * Hq > 0x7fffffffLL / 2)
+      (int64_t)total_q * Hq > 0x7fffffffLL / 2 || !map_strides(qs, 2))
     return SA_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dense_workspace_bytes(total_q, Hq, Hkv, D))
@@ -1249,6 +1264,7 @@ int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int 
   a->Hq = Hq;
   a->Hkv = Hkv;
   a->D = D;
+  a->tile_toks = dense_tile_toks(Hq / Hkv);
   a->window = window < (1 << 30) ? window : 0;   // positions stay below 2^30
   a->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   a->o = o;
@@ -1283,11 +1299,12 @@ int chunk_impl(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int to
   a.P_pool = P_pool;
   a.box = 16;
   while (a.box < 128 && page_size % (2 * a.box) == 0) a.box *= 2;
-  CUtensorMap kmap, vmap;
-  if (!encode_kv_map(&kmap, k_cache, D, page_size, Hkv, P_pool, ks, a.box) ||
+  CUtensorMap qmap, kmap, vmap;
+  if (!encode_q_map(&qmap, q, D, Hq, total_q, qs[0], qs[1], Hq / Hkv, a.tile_toks) ||
+      !encode_kv_map(&kmap, k_cache, D, page_size, Hkv, P_pool, ks, a.box) ||
       !encode_kv_map(&vmap, v_cache, D, page_size, Hkv, P_pool, vs, a.box))
     return SA_ERR_CUDA;
-  return cuda_status(launch_dense(a, kmap, vmap, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dense(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream)));
 }
 }  // namespace
 
@@ -1394,11 +1411,12 @@ int sa_prompt_attention(const uint16_t* q, const int64_t q_strides[3], const int
   const int64_t* ks = total_k > 0 ? k_strides : one;
   const int64_t* vs = total_k > 0 ? v_strides : one;
   const int64_t k4[4] = {ks[0], ks[1], ks[0], 1}, v4[4] = {vs[0], vs[1], vs[0], 1};
-  CUtensorMap kmap, vmap;
-  if (!encode_kv_map(&kmap, total_k > 0 ? k : q, D, rows, total_k > 0 ? Hkv : 1, 1, k4, 128) ||
+  CUtensorMap qmap, kmap, vmap;
+  if (!encode_q_map(&qmap, q, D, Hq, total_q, q_strides[0], q_strides[1], Hq / Hkv, a.tile_toks) ||
+      !encode_kv_map(&kmap, total_k > 0 ? k : q, D, rows, total_k > 0 ? Hkv : 1, 1, k4, 128) ||
       !encode_kv_map(&vmap, total_k > 0 ? v : q, D, rows, total_k > 0 ? Hkv : 1, 1, v4, 128))
     return SA_ERR_CUDA;
-  return cuda_status(launch_dense(a, kmap, vmap, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dense(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -6,8 +6,9 @@
 // sees the keys j at or before it (and, with a window, j > position - window):
 //   S = scale q.k_j,  O = sum_j softmax(S)_j v_j,  lse = log sum_j exp(S_j).
 // The rows of one (sequence, kv head) are (token, group head) pairs, token
-// major, so a K/V tile is read once for all heads of its group.  An item is 256
-// of these rows; its work is the 128-key tiles any of its rows sees.
+// major, so a K/V tile is read once for all heads of its group.  An item is two
+// tiles of these rows (each the whole tokens that fit 128 rows); its work is the
+// 128-key tiles any of its rows sees.
 //
 // Work split.  Every CTA (one per SM) takes an equal share of all items' tiles,
 // laid end to end (sequence, kv head, row tile), wherever the share's ends cut
@@ -28,7 +29,10 @@
 //                 QK_B(i+1): one tile's MMAs run under the other's softmax;
 //   warp 9        K and V tiles by TMA through the page map into two rings
 //                 (a missing page loads zeros from an out-of-range coordinate);
-//   warp 10       the next item's queries by cp.async as soon as its buffer frees.
+//   warp 10       the next item's queries by TMA as soon as their buffer frees (the
+//                 box is the group's heads of as many tokens as fit 128 rows);
+//   warp 11       plans the CTA's share, and zeroes the value rows past a
+//                 sequence's end.
 // An item of at most 128 rows gives both tiles the same rows and every other
 // key tile each ("halves"); the two running softmaxes merge in the epilogue,
 // both accumulators being in the same TMEM lanes.
@@ -36,6 +40,8 @@
 // P is one bf16 rounding of each probability (relative 2^-8 at most, the same
 // step as the bf16 output's own rounding); the row sums, and so the LSE, are of
 // the unrounded float32 probabilities.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc05.cuh"
@@ -52,6 +58,8 @@ constexpr int kItemUnits = 1;     // an item's fixed cost, in tiles
 constexpr int kMinUnits = 2;      // smallest share worth a CTA
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
+constexpr int kStageRow = 80;     // bytes: 64 + 16 against bank conflicts
+static_assert(kDenseMaxBatch * 4 <= kSoftWarps * 32 * kStageRow, "the units fit the stage");
 
 template <int D>
 struct Cfg {
@@ -63,7 +71,7 @@ struct Cfg {
   static constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kM, kKeys, false, false);
   static constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kM, D, false, true);
 };
-static_assert(kBadRing > 4 && kDenseRows == 2 * kM, "ring and item shapes");
+static_assert(kBadRing > 4, "more tiles than a ring and its consumers hold");
 
 // ---------------------------------------------------------------- geometry
 struct Seq {
@@ -90,17 +98,16 @@ SA_DEV Seq seq_of(const DenseArgs& a, int b, int32_t* err) {
   }
   return s;
 }
-// Key tiles [x, y) that some row of item qt sees (empty: x == y == 0).
-SA_DEV int2 tiles_of(const Seq& s, int G, int window, int qt) {
-  const int rows = s.n * G, r0 = qt * kDenseRows;
-  const int t_first = r0 / G, t_last = (min(rows, r0 + kDenseRows) - 1) / G;
+// Key tiles [x, y) that some row of item qt (toks tokens) sees (empty: x == y == 0).
+SA_DEV int2 tiles_of(const Seq& s, int toks, int window, int qt) {
+  const int t_first = qt * toks, t_last = min(s.n, t_first + toks) - 1;
   const int hi = min(s.L, s.L - s.n + t_last + 1);
   const int lo = window ? max(0, s.L - s.n + t_first - window + 1) : 0;
   if (hi <= lo) return make_int2(0, 0);
   return make_int2(lo / kKeys, (hi + kKeys - 1) / kKeys);
 }
-SA_DEV int item_units(const Seq& s, int G, int window, int qt) {
-  const int2 t = tiles_of(s, G, window, qt);
+SA_DEV int item_units(const Seq& s, int toks, int window, int qt) {
+  const int2 t = tiles_of(s, toks, window, qt);
   return kItemUnits + t.y - t.x;
 }
 
@@ -132,16 +139,21 @@ SA_DEV void cta_sync() { asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memo
 // 256 x 208 for the softmax warps (a row of scores is 128 registers) + 128 x 88.
 SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// A value every lane holds alike, as the compiler can see.
+template <typename T>
+SA_DEV T uni(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 SA_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ CUtensorMap kmap,
+    dense_kernel(const __grid_constant__ DenseArgs a, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   const int G = a.Hq / a.Hkv;
+  const int toks = 2 * a.tile_toks, tile_rows = a.tile_toks * G;   // tokens of an item, rows of a tile
 
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* smem = dyn_smem + ((1024 - (smem_u32(dyn_smem) & 1023)) & 1023);
@@ -151,10 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t k_full[C::kStages], k_empty[C::kStages];
   __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages];
   __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty;
+  __shared__ uint64_t v_tail, v_tail_seen;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, n_segs_s, last_s;
   __shared__ Seg seg_s[kMaxSegs];
-  __shared__ uint32_t units_s[kDenseMaxBatch];
+  // per softmax warp: 32 rows x 64 bytes of output on their way to global memory
+  // (first, until the first segments are planned, the units of every sequence)
+  __shared__ __align__(16) uint8_t stage_s[kSoftWarps][32 * kStageRow];
+  uint32_t* units_s = reinterpret_cast<uint32_t*>(stage_s);
   __shared__ uint32_t bad_s[kBadRing];
   __shared__ float2 ml_s[2][kM];
   volatile int* abort_flag = &abort_s;
@@ -169,26 +185,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&s_full[w], 2);
+      mbar_init(&s_full[w], 1);
       mbar_init(&p_full[w][0], 4);
       mbar_init(&p_full[w][1], 4);
       mbar_init(&o_done[w], 1);
     }
-    mbar_init(&q_full, 32);
+    mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
+    mbar_init(&v_tail, 32);
+    mbar_init(&v_tail_seen, 1);
     abort_s = 0;
     fence_mbar_init();
     a.part_head[cta * 8] = 0;   // no part of this CTA starts an item, so far
   }
   if (warp == kLoadWarp && lane == 0) {
+    prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
   }
   for (int b = warp; b < a.B; b += kThreads / 32) {
     const Seq s = seq_of(a, b, cta == 0 && lane == 0 ? a.err : nullptr);
-    const int nqt = (s.n * G + kDenseRows - 1) / kDenseRows;
+    const int nqt = (s.n + toks - 1) / toks;
     uint32_t u = 0;
-    for (int qt = lane; qt < nqt; qt += 32) u += item_units(s, G, a.window, qt);
+    for (int qt = lane; qt < nqt; qt += 32) u += item_units(s, toks, a.window, qt);
     u = __reduce_add_sync(0xffffffffu, u);
     if (lane == 0) units_s[b] = u;
   }
@@ -198,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base_s;
 
   uint32_t kc = 0;                  // key tiles so far
-  uint32_t cw[2] = {0, 0};          // S / P hand-overs so far, per tile
-  uint32_t oc[2] = {0, 0};          // accumulators finished so far, per tile
+  uint32_t cw0 = 0, cw1 = 0;        // S / P hand-overs so far, per tile (softmax: its own, cw0)
+  uint32_t oc0 = 0, oc1 = 0;        // accumulators finished so far: this tile's, the other's
   uint32_t qc = 0;                  // query loads so far
   bool ok = true;
 
@@ -221,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n_segs; ++i) {
         const Seg s = seg_s[i];
         const int nt = s.j1 - s.j0;
-        const bool halves = s.nr <= kM;
+        const bool halves = s.nr <= tile_rows;
         const int n_w = halves ? (w ? nt / 2 : (nt + 1) / 2) : nt;
         const int n_other = halves ? (w ? (nt + 1) / 2 : nt / 2) : nt;
-        const int rr = (halves ? 0 : w * kM) + row;
-        const bool row_ok = rr < s.nr;
+        const int rr = (halves ? 0 : w * tile_rows) + row;
+        const bool row_ok = row < tile_rows && rr < s.nr;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         const int rg = s.r0 + rr;
         const int t = row_ok ? rg / G : 0;
@@ -235,10 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vis_hi = min(s.L, qpos + 1);
         const int vis_lo = a.window ? qpos - a.window + 1 : 0;
         float m_ref = -INFINITY, l = 0.f;
-        for (int it = 0; it < n_w; ++it, ++cw[0]) {
+        for (int it = 0; it < n_w; ++it, ++cw0) {
           const int ti = halves ? 2 * it + w : it;
           const int k0 = (s.j0 + ti) * kKeys;
-          ok = ok && warp_wait(&s_full[w], cw[0] & 1, abort_flag);
+          ok = ok && warp_wait(&s_full[w], cw0 & 1, abort_flag);
           if (!ok) break;
           if (!warp_ok) {   // no rows here: whatever P holds reaches no row that is kept
             __syncwarp();
@@ -249,51 +268,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           tc::fence_after_sync();
-          float x[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tc::ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
           const int lo = vis_lo - k0, hi = vis_hi - k0;
           const uint32_t bad = bad_s[(kc + ti) % kBadRing];
           const bool masked =
               __any_sync(0xffffffffu, bad || (row_ok && (lo > 0 || hi < kKeys)));
-          tc::wait_ld();
-          if (masked) {
+          float x[128], m_new = m_ref;
+          for (bool moved = false;;) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t vis = hi >= 32 * c + 32 ? 0xffffffffu
-                                               : hi > 32 * c ? (1u << (hi - 32 * c)) - 1u : 0u;
-              if (lo > 32 * c)
-                vis &= lo >= 32 * c + 32 ? 0u : ~((1u << (lo - 32 * c)) - 1u);
-              if (bad) {
+            for (int c = 0; c < 4; ++c)
+              tc::ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
+            tc::wait_ld();
+            if (masked) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if ((bad >> ((32 * c + 16 * h) >> boxes_log2)) & 1u) vis &= ~(0xffffu << (16 * h));
+              for (int c = 0; c < 4; ++c) {
+                uint32_t vis = hi >= 32 * c + 32 ? 0xffffffffu
+                                                 : hi > 32 * c ? (1u << (hi - 32 * c)) - 1u : 0u;
+                if (lo > 32 * c)
+                  vis &= lo >= 32 * c + 32 ? 0u : ~((1u << (lo - 32 * c)) - 1u);
+                if (bad) {
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if ((bad >> ((32 * c + 16 * h) >> boxes_log2)) & 1u)
+                      vis &= ~(0xffffu << (16 * h));
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((vis >> k) & 1u)) x[32 * c + k] = -INFINITY;
               }
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((vis >> k) & 1u)) x[32 * c + k] = -INFINITY;
             }
-          }
-          const float mx = reduce_n<false>(x) * sl;
-          const bool move = mx > m_ref + kLazy;
-          const float m_new = move ? mx : m_ref;
-          const float nb = m_new == -INFINITY ? 0.f : -m_new;
-          if (__any_sync(0xffffffffu, move)) {
+            if (moved) break;
+            const float mx = reduce_n<false>(x) * sl;
+            const bool move = mx > m_ref + kLazy;
+            if (!__any_sync(0xffffffffu, move)) break;
             const float alpha = move ? exp2f(m_ref - mx) : 1.f;
+            m_new = move ? mx : m_ref;
             l *= alpha;
-            if (it > 0) {   // this row's PV of the previous tile is complete
+            if (it == 0) break;
+            // this row's PV of the previous tile is complete; the scores are
+            // read again afterwards, so that they hold no registers meanwhile
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tc::ld32(o_col + c * 32, o);
-                tc::wait_ld();
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tc::ld32(o_col + c * 32, o);
+              tc::wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                tc::st32(o_col + c * 32, o);
-              }
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tc::st32(o_col + c * 32, o);
             }
+            moved = true;
           }
+          const float nb = m_new == -INFINITY ? 0.f : -m_new;
           m_ref = m_new;
           unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
           const unsigned long long sl2 = f2_pack(sl, sl), nb2 = f2_pack(nb, nb);
@@ -321,15 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- epilogue
         if (n_w > 0) {
-          ok = ok && warp_wait(&o_done[w], oc[0] & 1, abort_flag);
-          ++oc[0];
+          ok = ok && warp_wait(&o_done[w], oc0 & 1, abort_flag);
+          ++oc0;
         }
         float wa = 1.f, wb = 0.f, m_all = m_ref, l_all = l;
         const int id = 1 + quarter;
         if (halves) {   // the other half's running max and sum, and its accumulator
           if (n_other > 0) {
-            ok = ok && warp_wait(&o_done[1 - w], oc[1] & 1, abort_flag);
-            ++oc[1];
+            ok = ok && warp_wait(&o_done[1 - w], oc1 & 1, abort_flag);
+            ++oc1;
           }
           ml_s[w][row] = make_float2(m_ref, l);
           pair_sync(id);
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wb = other.x == -INFINITY ? 0.f : exp2f(other.x - m_all);
           l_all = l * wa + other.y * wb;
         } else {
-          if (nt > 0) ++oc[1];
+          if (nt > 0) ++oc1;
         }
         tc::fence_after_sync();
         const bool empty = !ok || l_all == 0.f;
@@ -348,8 +372,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         wb *= inv;
         const bool use_a = n_w > 0, use_b = halves && n_other > 0;
         const uint32_t b_col = tmem + lanes + 256 + D * (1 - w);
-        const int64_t orow = (int64_t)(s.q0 + t) * a.Hq + head;
+        const int orow = (s.q0 + t) * a.Hq + head;
         if (warp_ok) {
+          // The rows leave through shared memory, 64 bytes of each at a time, so
+          // that a store covers whole sectors.  Lane 4 r + p of a store holds
+          // piece p of rows r, 8 + r, 16 + r, 24 + r.
+          uint8_t* stage = stage_s[warp];
+          const int mine = !row_ok ? -1 : s.part < 0 ? orow : s.part * a.rows_cap + rr;
+          int dst_row[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst_row[k] = __shfl_sync(0xffffffffu, mine, 8 * k + (lane >> 2));
+          uint8_t* dst = s.part < 0 ? reinterpret_cast<uint8_t*>(a.o)
+                                    : reinterpret_cast<uint8_t*>(a.part_o);
+          const int64_t row_bytes = s.part < 0 ? D * 2 : D * 4;
+          auto flush = [&](int byte0) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  stage + (8 * k + (lane >> 2)) * kStageRow + (lane & 3) * 16);
+              if (dst_row[k] >= 0)
+                *reinterpret_cast<uint4*>(dst + dst_row[k] * row_bytes + byte0 + (lane & 3) * 16) =
+                    v;
+            }
+            __syncwarp();
+          };
+          uint4* own = reinterpret_cast<uint4*>(stage + lane * kStageRow);
           // halves: each of the two threads of a row writes half of the columns
           const int c0 = halves ? w * (D / 64) : 0, c1 = halves ? c0 + D / 64 : D / 32;
           for (int c = c0; c < c1; ++c) {
@@ -374,21 +423,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = 0.f;
             }
-            if (row_ok) {
-              if (s.part < 0) {
-                uint4* dst = reinterpret_cast<uint4*>(a.o + orow * D + c * 32);
+            if (s.part < 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                own[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]),
+                                    pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                    pack_bf16(o[8 * k + 4], o[8 * k + 5]),
+                                    pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+              flush(c * 64);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]),
-                                      pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                                      pack_bf16(o[8 * k + 4], o[8 * k + 5]),
-                                      pack_bf16(o[8 * k + 6], o[8 * k + 7]));
-              } else {
-                float4* dst = reinterpret_cast<float4*>(
-                    a.part_o + ((int64_t)s.part * a.rows_cap + rr) * D + c * 32);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                  own[k] = make_uint4(__float_as_uint(o[16 * h + 4 * k]),
+                                      __float_as_uint(o[16 * h + 4 * k + 1]),
+                                      __float_as_uint(o[16 * h + 4 * k + 2]),
+                                      __float_as_uint(o[16 * h + 4 * k + 3]));
+                flush(c * 128 + h * 64);
               }
             }
           }
@@ -467,131 +519,131 @@ __global__ void __launch_bounds__(kThreads, 1)
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
-        constexpr int kPieces = D / 8, kStep = 32 / kPieces;   // rows per pass of the warp
-        const int pc = lane % kPieces;
         for (int i = 0; i < n_segs && ok; ++i) {
-          const Seg s = seg_s[i];
+          const Seg& s = seg_s[i];
           if (s.j0 == s.j1) continue;
           if (qc > 0 && !warp_wait(&q_empty, (qc - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          int row = lane / kPieces;
-          int t = (s.r0 + row) / G, h = (s.r0 + row) % G;
-          const uint16_t* base = a.q + s.q0 * a.q0 + (int64_t)s.kvh * G * a.q1 + pc * 8;
-          for (; row < s.nr; row += kStep) {
-            const int r = row & (kM - 1);
-            const uint32_t dst = smem_u32(q_s) + (row / kM) * C::kQBytes + (pc >> 3) * (kM * 128) +
-                                 r * 128 + (((pc & 7) ^ (r & 7)) << 4);
-            cp_async16(dst, base + t * a.q0 + h * a.q1, 16);
-            for (h += kStep; h >= G; h -= G) ++t;
+          // one box per tile and 64-column chunk; rows of other sequences' tokens
+          // that a box holds are never kept, tokens past the tensor load as zeros
+          const int tiles = s.nr > tile_rows ? 2 : 1;
+          if (lane == 0) mbar_arrive_expect_tx(&q_full, tiles * C::kChunks * tile_rows * 128);
+          __syncwarp();
+          if (lane < tiles * C::kChunks) {
+            const int w = lane / C::kChunks, ch = lane % C::kChunks;
+            tma_load_4d(q_s + w * C::kQBytes + ch * (kM * 128), &qmap, &q_full, ch * 64,
+                        s.kvh * G, s.q0 + s.r0 / G + w * a.tile_toks, 0);
           }
-          cp_async_commit();
-          cp_async_wait<0>();
-          tc::fence_proxy_async();
-          mbar_arrive(&q_full);
           ++qc;
         }
         cta_sync();
       }
     } else if (warp == kMmaWarp) {
-      // ================= MMA issue
+      // ================= MMA issue: warp-uniform code, one elected lane issues
+      const std::integral_constant<int, 0> A{};
+      const std::integral_constant<int, 1> B{};
+      const uint32_t q_desc = uni(tc::desc_lo(smem_u32(q_s), 16));
+      const uint32_t k_desc = uni(tc::desc_lo(smem_u32(k_s), 16));
+      const uint32_t v_desc = uni(tc::desc_lo(smem_u32(v_s), kKeys * 128));
+      const uint32_t tmem_u = uni(tmem);
+      uint32_t tails = 0;
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
-        const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(k_s), v_addr = smem_u32(v_s);
-        for (int i = 0; i < n_segs && ok; ++i) {
-          const Seg s = seg_s[i];
-          const int nt = s.j1 - s.j0;
-          if (nt == 0) continue;
-          const bool halves = s.nr <= kM;
-          const int n_w[2] = {halves ? (nt + 1) / 2 : nt, halves ? nt / 2 : nt};
-          int qk_left = n_w[0] + n_w[1];
-          const int t_last = (s.r0 + s.nr - 1) / G;
-          const int hi = min(s.L, s.L - s.n + t_last + 1);
-          auto tile = [&](int it, int w) { return halves ? 2 * it + w : it; };
-          auto qk = [&](int it, int w) {
-            const uint32_t c = kc + tile(it, w);
-            const int st = c % C::kStages;
-            if (halves || w == 0) {
-              if (!warp_wait(&k_full[st], (c / C::kStages) & 1, abort_flag)) return false;
-              tc::fence_after_sync();
-            }
-            if (lane == 0) {
-              const uint32_t qb = q_addr + (halves ? 0 : w) * C::kQBytes;
-              const uint32_t kb = k_addr + st * C::kTileBytes;
-  #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = (kk >> 2) * (kM * 128) + (kk & 3) * 32;
-                tc::mma_bf16(tmem + 128 * w, tc::sdesc_sw128(qb + o, 16, 1024),
-                             tc::sdesc_sw128(kb + o, 16, 1024), C::kIdQK, kk > 0 ? 1u : 0u);
+        {
+          for (int i = 0; i < n_segs && ok; ++i) {
+            const Seg& s = seg_s[i];
+            const int j0 = uni(s.j0), nt = uni(s.j1) - j0, L = uni(s.L), nr = uni(s.nr);
+            if (nt == 0) continue;
+            const bool halves = nr <= tile_rows;
+            const int n_a = halves ? (nt + 1) / 2 : nt, n_b = halves ? nt / 2 : nt;
+            int qk_left = n_a + n_b;
+            const int hi = uni(min(L, L - s.n + (s.r0 + nr - 1) / G + 1));
+            auto qk = [&](int it, auto wc) {
+              constexpr int w = decltype(wc)::value;
+              const uint32_t c = kc + (halves ? 2 * it + w : it);
+              const int st = c % C::kStages;
+              if (halves || w == 0) {
+                if (!warp_wait(&k_full[st], (c / C::kStages) & 1, abort_flag)) return false;
+                tc::fence_after_sync();
               }
-              tc::commit(&s_full[w]);
-              mbar_arrive(&s_full[w]);   // releases bad_s to the softmax warps
-              if (halves || w == 1) tc::commit(&k_empty[st]);
-              if (qk_left == 1) tc::commit(&q_empty);
-            }
-            --qk_left;
-            return true;
-          };
-          auto pv = [&](int it, int w) {
-            const uint32_t c = kc + tile(it, w);
-            const int st = c % C::kStages, j = s.j0 + tile(it, w);
-            // 16-key steps some row of the item sees
-            const int steps = min(8, (hi - j * kKeys + 15) / 16);
-            for (int h = 0; h < 2; ++h) {
-              if (!warp_wait(&p_full[w][h], cw[w] & 1, abort_flag)) return false;
-              if (h == 0 && (halves || w == 0)) {
-                if (!warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag)) return false;
-                // value rows past the sequence's end may hold anything: 0 * NaN
-                const int z0 = max(0, s.L - j * kKeys), nz = 16 * steps - z0;
-                if (nz > 0) {
-                  uint8_t* vt = v_s + st * C::kTileBytes;
-                  for (int x = lane; x < nz * C::kChunks * 8; x += 32) {
-                    const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
-                    *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 +
-                                              (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+              if (tc::elect_one()) {
+                const uint32_t qd = q_desc + ((halves ? 0 : w) * C::kQBytes >> 4);
+                const uint32_t kd = k_desc + st * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t o = ((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4;
+                  tc::mma_bf16_lo(tmem_u + 128 * w, qd + o, kd + o, C::kIdQK, kk > 0 ? 1u : 0u);
+                }
+                tc::commit(&s_full[w]);
+                if (halves || w == 1) tc::commit(&k_empty[st]);
+                if (qk_left == 1) tc::commit(&q_empty);
+              }
+              __syncwarp();
+              --qk_left;
+              return true;
+            };
+            auto pv = [&](int it, auto wc) {
+              constexpr int w = decltype(wc)::value;
+              const int ti = halves ? 2 * it + w : it;
+              const uint32_t c = kc + ti;
+              const int st = c % C::kStages, j = j0 + ti;
+              // 16-key steps some row of the item sees
+              const int steps = min(8, (hi - j * kKeys + 15) / 16);
+              const uint32_t vd = v_desc + st * (C::kTileBytes >> 4);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!warp_wait(&p_full[w][h], (w ? cw1 : cw0) & 1, abort_flag)) return false;
+                if (h == 0 && (halves || w == 0)) {
+                  if (!warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag)) return false;
+                  if (L - j * kKeys < 16 * steps) {   // rows past the end: zeroed first
+                    if (!warp_wait(&v_tail, tails & 1, abort_flag)) return false;
+                    if (lane == 0) mbar_arrive(&v_tail_seen);
+                    ++tails;
                   }
-                  tc::fence_proxy_async();
-                  __syncwarp();
                 }
-              }
-              tc::fence_after_sync();
-              if (lane == 0) {
-                const uint32_t vb = v_addr + st * C::kTileBytes;
-  #pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                  const int kk = 4 * h + k4;
-                  if (kk < steps)
-                    tc::mma_bf16_ts(tmem + 256 + D * w, tmem + 128 * w + 8 * kk,
-                                    tc::sdesc_sw128(vb + kk * 2048, kKeys * 128, 1024), C::kIdPV,
-                                    (it > 0 || kk > 0) ? 1u : 0u);
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+#pragma unroll
+                  for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                    if (kk < steps)
+                      tc::mma_bf16_ts_lo(tmem_u + 256 + D * w, tmem_u + 128 * w + 8 * kk,
+                                         vd + kk * (2048 >> 4), C::kIdPV,
+                                         (it > 0 || kk > 0) ? 1u : 0u);
                 }
+                __syncwarp();
               }
+              w ? ++cw1 : ++cw0;
+              if ((halves || w == 1) && tc::elect_one()) tc::commit(&v_empty[st]);
+              __syncwarp();
+              return true;
+            };
+            ok = warp_wait(&q_full, qc & 1, abort_flag);
+            tc::fence_after_sync();
+            ok = ok && qk(0, A) && (n_b == 0 || qk(0, B));
+            for (int it = 0; ok && it < n_a; ++it) {
+              ok = pv(it, A);
+              if (ok && it + 1 < n_a)
+                ok = qk(it + 1, A);
+              else if (tc::elect_one())
+                tc::commit(&o_done[0]);
+              __syncwarp();
+              if (!ok || it >= n_b) continue;
+              ok = pv(it, B);
+              if (ok && it + 1 < n_b)
+                ok = qk(it + 1, B);
+              else if (tc::elect_one())
+                tc::commit(&o_done[1]);
+              __syncwarp();
             }
-            ++cw[w];
-            if (lane == 0 && (halves || w == 1)) tc::commit(&v_empty[st]);
-            return true;
-          };
-          ok = warp_wait(&q_full, qc & 1, abort_flag);
-          tc::fence_after_sync();
-          ok = ok && qk(0, 0) && (n_w[1] == 0 || qk(0, 1));
-          for (int it = 0; ok && it < n_w[0]; ++it) {
-  #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (!ok || it >= n_w[w]) continue;
-              ok = pv(it, w);
-              if (!ok) continue;
-              if (it + 1 < n_w[w])
-                ok = qk(it + 1, w);
-              else if (lane == 0)
-                tc::commit(&o_done[w]);
-            }
+            kc += nt;
+            ++qc;
           }
-          kc += nt;
-          ++qc;
         }
+        __syncwarp();
         cta_sync();
       }
     } else if (warp == kPlanWarp) {
@@ -635,10 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           off -= (int64_t)ckvh * units_s[cb];
           // the row tile: 32 at a time
           const Seq s = seq_of(a, cb, nullptr);
-          const int nqt = (s.n * G + kDenseRows - 1) / kDenseRows;
+          const int nqt = (s.n + toks - 1) / toks;
           for (int q0 = 0; q0 < nqt; q0 += 32) {
             const int qt = q0 + lane;
-            int incl = qt < nqt ? item_units(s, G, a.window, qt) : 0;
+            int incl = qt < nqt ? item_units(s, toks, a.window, qt) : 0;
             const int own = incl;
             for (int o = 1; o < 32; o <<= 1) {
               const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -654,16 +706,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             off -= __shfl_sync(0xffffffffu, incl, 31);
           }
         }
+      uint32_t tails = 0;
+      bool last = false;
       do {
         // the next segments
         if (lane == 0) {
           int ns = 0;
           while (w_pos < w_hi && ns < kMaxSegs && cb < a.B) {
             const Seq s = seq_of(a, cb, nullptr);
-            const int rows = s.n * G;
-            const int nqt = (rows + kDenseRows - 1) / kDenseRows;
+            const int nqt = (s.n + toks - 1) / toks;
             while (w_pos < w_hi && ns < kMaxSegs && ckvh < a.Hkv && nqt > 0) {
-              const int2 t = tiles_of(s, G, a.window, cqt);
+              const int2 t = tiles_of(s, toks, a.window, cqt);
               const int nt = t.y - t.x, units = kItemUnits + nt;
               const int ua = (int)c_off;
               const int ub = (int)min((int64_t)units, c_off + (w_hi - w_pos));
@@ -673,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Seg& g = seg_s[ns++];
                 g.q0 = s.q0, g.n = s.n, g.k0 = s.k0, g.L = s.L;
                 g.b = cb, g.kvh = ckvh;
-                g.r0 = cqt * kDenseRows;
-                g.nr = min(kDenseRows, rows - g.r0);
+                g.r0 = cqt * toks * G;
+                g.nr = min(toks, s.n - cqt * toks) * G;
                 g.j0 = t.x + ta, g.j1 = t.x + tb;
                 g.part = -1;
                 if (ta > 0 || tb < nt) {
@@ -697,9 +750,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           n_segs_s = ns;
           last_s = w_pos >= w_hi || cb >= a.B;
         }
+        __syncwarp();
         cta_sync();
+        // value rows past a sequence's end may hold anything (0 * NaN): zeroed in
+        // the tile, up to the 16-key step that is multiplied
+        last = last_s;
+        const int n_segs = n_segs_s;
+        for (int i = 0; i < n_segs && ok; ++i) {
+          const Seg& s = seg_s[i];
+          const int nt = s.j1 - s.j0, j = s.j1 - 1;
+          const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
+          const int rows = 16 * min(8, (hi - j * kKeys + 15) / 16), z0 = s.L - j * kKeys;
+          if (nt > 0 && z0 < rows) {
+            const uint32_t c = kc + nt - 1;
+            const int st = c % C::kStages;
+            ok = warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag);
+            uint8_t* vt = v_s + st * C::kTileBytes;
+            for (int x = lane; x < (rows - z0) * C::kChunks * 8; x += 32) {
+              const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
+              *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 + (p & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async();
+            // one tail at a time: v_tail has a single phase to wait for
+            if (tails > 0) ok = ok && warp_wait(&v_tail_seen, (tails - 1) & 1, abort_flag);
+            mbar_arrive(&v_tail);
+            ++tails;
+          }
+          kc += nt;
+        }
         cta_sync();
-      } while (!last_s);
+      } while (!last);
     }
   }
   if (warp == kLoadWarp && abort_s) {
@@ -767,15 +848,15 @@ __global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant_
 }
 
 template <int D>
-cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                     cudaStream_t stream) {
+cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                     const CUtensorMap& vmap, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   e = allow_max_dyn_smem(reinterpret_cast<const void*>(dense_kernel<D>));
   if (e != cudaSuccess) return e;
   const int ctas = sms < kDenseMaxCtas ? sms : kDenseMaxCtas;
-  dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, kmap, vmap);
+  dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, qmap, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int by = (a.rows_cap + 31) / 32;   // 32 rows per block
@@ -784,13 +865,14 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& kmap, const CUtensor
 }
 
 int rows_cap_of(int total_q, int Hq, int Hkv) {
-  const int64_t rows = (int64_t)total_q * (Hq / Hkv);
-  return (int)(rows < kDenseRows ? rows : kDenseRows);
+  const int G = Hq / Hkv, item = 2 * dense_tile_toks(G);
+  return (total_q < item ? total_q : item) * G;
 }
 size_t r16(size_t x) { return (x + 15) / 16 * 16; }
 
 }  // namespace
 
+int dense_tile_toks(int G) { return kM / G; }
 size_t dense_workspace_bytes(int total_q, int Hq, int Hkv, int D) {
   const size_t rows = 2 * (size_t)kDenseMaxCtas * rows_cap_of(total_q, Hq, Hkv);
   return kDenseMaxCtas * 32 + r16(rows * 4) + rows * D * 4;
@@ -804,11 +886,11 @@ void dense_workspace(DenseArgs* a, void* ws) {
   a->part_o = reinterpret_cast<float*>(p + kDenseMaxCtas * 32 + r16(rows * 4));
 }
 
-cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                         cudaStream_t stream) {
+cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, cudaStream_t stream) {
   switch (a.D) {
-    case 64: return launch_d<64>(a, kmap, vmap, stream);
-    case 128: return launch_d<128>(a, kmap, vmap, stream);
+    case 64: return launch_d<64>(a, qmap, kmap, vmap, stream);
+    case 128: return launch_d<128>(a, qmap, kmap, vmap, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -260,6 +260,7 @@ struct DenseArgs {
   const int32_t* seq_lens; // [B] (paged)
   int B, total_q, Hq, Hkv, D, P, P_pool;
   int box;                 // rows of a K / V load: divides the page size and 128
+  int tile_toks;           // tokens of a 128-row query tile: dense_tile_toks(Hq / Hkv)
   int window;              // 0: every earlier key
   float scale_log2;
   uint16_t* o;             // [total_q, Hq, D]
@@ -273,12 +274,16 @@ struct DenseArgs {
 };
 constexpr int kDenseMaxCtas = 160;    // persistent CTAs of a launch, at most
 constexpr int kDenseMaxBatch = 4096;  // sequences
-constexpr int kDenseRows = 256;       // query rows (tokens x heads of a group) of an item
+int dense_tile_toks(int G);           // whole tokens (of G heads) in a query tile
 size_t dense_workspace_bytes(int total_q, int Hq, int Hkv, int D);
 // Point the workspace fields of `a` into `ws`.
 void dense_workspace(DenseArgs* a, void* ws);
-cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                         cudaStream_t stream);
+cudaError_t launch_dense(const DenseArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, cudaStream_t stream);
+// Tensor map of packed queries [total, Hq, D]: 64-column boxes of G heads of
+// `toks` tokens, 128-byte swizzle.  false on failure.
+bool encode_q_map(CUtensorMap* map, const void* base, int D, int Hq, int total, int64_t tok_stride,
+                  int64_t head_stride, int G, int toks);
 
 // Packed new tokens (sequence b: tokens cu[b] .. cu[b + 1] - 1) rotated into
 // the paged cache, and the queries with them.
