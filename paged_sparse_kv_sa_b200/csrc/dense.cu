@@ -27,12 +27,12 @@
 //   warp 8        issues tcgen05.mma: S_w = Q_w K^T (M 128, N 128), O_w += P_w V
 //                 with P from TMEM, in the order PV_A(i), QK_A(i+1), PV_B(i),
 //                 QK_B(i+1): one tile's MMAs run under the other's softmax;
-//   warp 9        K and V tiles by TMA through the page map into two rings
-//                 (a missing page loads zeros from an out-of-range coordinate);
+//   warps 9, 11   K, V tiles by TMA through the page map into a ring each (a
+//                 missing page loads zeros from an out-of-range coordinate);
 //   warp 10       the next item's queries by TMA as soon as their buffer frees (the
 //                 box is the group's heads of as many tokens as fit 128 rows);
-//   warp 11       plans the CTA's share, and zeroes the value rows past a
-//                 sequence's end.
+//                 it also zeroes the value rows past a sequence's end;
+//   warp 11       first plans the CTA's share.
 // An item of at most 128 rows gives both tiles the same rows and every other
 // key tile each ("halves"); the two running softmaxes merge in the epilogue,
 // both accumulators being in the same TMEM lanes.
@@ -106,6 +106,11 @@ SA_DEV int2 tiles_of(const Seq& s, int toks, int window, int qt) {
   if (hi <= lo) return make_int2(0, 0);
   return make_int2(lo / kKeys, (hi + kKeys - 1) / kKeys);
 }
+// a / b, in 32 bits where both fit.
+SA_DEV int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 SA_DEV int item_units(const Seq& s, int toks, int window, int qt) {
   const int2 t = tiles_of(s, toks, window, qt);
   return kItemUnits + t.y - t.x;
@@ -121,10 +126,19 @@ struct Seg {
 };
 
 // ---------------------------------------------------------------- waits
+constexpr uint64_t kPatience = 1000000000ull;   // ns; no copy or product takes near as long
+SA_DEV uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Wait for phase `parity`; gives up after kPatience, or when another role has.
 SA_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 1023u && *abort_flag) return false;
+    if ((i & 255u) == 0 && (*abort_flag || now_ns() - t0 > kPatience)) break;
   }
   *abort_flag = 1;
   return false;
@@ -143,6 +157,72 @@ SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 template <typename T>
 SA_DEV T uni(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 SA_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// Largest of three, or of two (NaN if one is).
+SA_DEV float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+SA_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Largest of x[i0 .. i0 + 63], four chains.
+SA_DEV float max64(const float (&x)[128], int i0) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = max3_nan(x[i0 + i], x[i0 + 4 + i], x[i0 + 8 + i]);
+#pragma unroll
+  for (int c = 12; c < 60; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max3_nan(m[i], x[i0 + c + i], x[i0 + c + 4 + i]);
+  m[0] = max3_nan(m[0], x[i0 + 60], x[i0 + 61]);
+  m[1] = max3_nan(m[1], x[i0 + 62], x[i0 + 63]);
+  return max3_nan(m[0], m[1], max_nan(m[2], m[3]));
+}
+
+// Where lane's box of key tile j comes from: a tile is kKeys / box boxes (lane mod
+// their number) by D / 64 column chunks (lane / their number).
+struct Box {
+  int page, row;
+  uint32_t bad;   // boxes on pages that are not in the pool (all lanes)
+};
+SA_DEV Box box_of(const DenseArgs& a, const Seg& s, int j, int lane) {
+  const int nb = kKeys / a.box;
+  const int key = j * kKeys + (lane & (nb - 1)) * a.box;
+  Box x = {0, s.k0 + key, 0};
+  bool bad = false;
+  if (!a.cu_k) {
+    x.page = a.P_pool;   // out of range: zeros
+    x.row = 0;
+    if (key < s.L) {
+      const int ph = page_at(a.pt, s.b, key / a.P);
+      bad = ph < 0 || ph >= a.P_pool;
+      if (!bad) x.page = ph, x.row = key % a.P;
+    }
+  }
+  x.bad = __ballot_sync(0xffffffffu, bad) & ((1u << nb) - 1u);
+  return x;
+}
+// Load the c-th tile of a ring, once its stage is free; the whole warp.
+template <int D>
+SA_DEV bool load_tile(const Box& x, int kvh, uint32_t c, uint8_t* ring, const CUtensorMap* map,
+                      uint64_t* full, uint64_t* empty, int box, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31, nb = kKeys / box, st = c % C::kStages;
+  if (c >= (uint32_t)C::kStages &&
+      !warp_wait(&empty[st], ((c / C::kStages) - 1) & 1, abort_flag))
+    return false;
+  if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+  __syncwarp();
+  const int g = lane & (nb - 1), ch = lane / nb;
+  if (ch < C::kChunks)
+    tma_load_4d(ring + st * C::kTileBytes + ch * (kKeys * 128) + g * box * 128, map, &full[st],
+                ch * 64, x.row, kvh, x.page);
+  return true;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -274,11 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __any_sync(0xffffffffu, bad || (row_ok && (lo > 0 || hi < kKeys)));
           float x[128], m_new = m_ref;
           for (bool moved = false;;) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tc::ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
-            tc::wait_ld();
-            if (masked) {
+            auto hide = [&] {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 uint32_t vis = hi >= 32 * c + 32 ? 0xffffffffu
@@ -295,10 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 32; ++k)
                   if (!((vis >> k) & 1u)) x[32 * c + k] = -INFINITY;
               }
-            }
+            };
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tc::ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
+            tc::wait_ld();
+            if (masked) hide();
             if (moved) break;
-            const float mx = reduce_n<false>(x) * sl;
-            const bool move = mx > m_ref + kLazy;
+            // (a NaN score makes the row's maximum, and so the row, NaN)
+            const float mx = max_nan(max64(x, 0), max64(x, 64)) * sl;
+            const bool move = !(mx <= m_ref + kLazy);
             if (!__any_sync(0xffffffffu, move)) break;
             const float alpha = move ? exp2f(m_ref - mx) : 1.f;
             m_new = move ? mx : m_ref;
@@ -333,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[k] = pack_bf16(p0, p1);
             }
             tc::st16(s_col + 16 * c, p);
-            if (c & 1) {
+            if (c & 1) {   // 64 keys
               tc::wait_st();
               tc::fence_before_sync();
               __syncwarp();
@@ -399,30 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           };
           uint4* own = reinterpret_cast<uint4*>(stage + lane * kStageRow);
-          // halves: each of the two threads of a row writes half of the columns
-          const int c0 = halves ? w * (D / 64) : 0, c1 = halves ? c0 + D / 64 : D / 32;
-          for (int c = c0; c < c1; ++c) {
-            float o[32];
-            if (use_a) {
-              tc::ld32(o_col + c * 32, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= wa;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            }
-            if (use_b) {
-              float ob[32];
-              tc::ld32(b_col + c * 32, ob);
-              tc::wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = fmaf(ob[k], wb, o[k]);
-            }
-            if (empty) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            }
+          // 32 columns (o, final) of every row, columns 32 c ..
+          auto put = [&](const float* o, int c) {
             if (s.part < 0) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -443,6 +503,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 flush(c * 128 + h * 64);
               }
             }
+          };
+          // 64 columns' loads in flight together: a tile's own, or (halves: each of
+          // the two threads of a row writes half of the columns) 32 of each tile's
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            float o[64];
+            float(&oa)[32] = *reinterpret_cast<float(*)[32]>(&o[0]);
+            float(&ob)[32] = *reinterpret_cast<float(*)[32]>(&o[32]);
+            const int ca = halves ? w * (D / 64) + c : 2 * c;
+            tc::ld32(o_col + ca * 32, oa);
+            tc::ld32(halves ? b_col + ca * 32 : o_col + ca * 32 + 32, ob);
+            tc::wait_ld();
+            if (halves) {   // (an accumulator that was never written may hold anything)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float x = use_a ? oa[k] * wa : 0.f;
+                oa[k] = empty ? 0.f : use_b ? fmaf(ob[k], wb, x) : x;
+              }
+              put(oa, ca);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 64; ++k) o[k] = empty || !use_a ? 0.f : o[k] * wa;
+              put(oa, ca);
+              put(ob, ca + 1);
+            }
           }
           if (row_ok && !(halves && w)) {
             const float lse2 = empty ? -INFINITY : m_all + log2f(l_all);
@@ -462,66 +547,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_down();
     if (warp == kLoadWarp) {
-      // ================= K and V tiles
+      // ================= K tiles
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
-        const int nb = kKeys / a.box;
-        const int g = lane & (nb - 1), ch = lane / nb;   // box and 64-column chunk of this lane
         for (int i = 0; i < n_segs && ok; ++i) {
           const Seg s = seg_s[i];
-          for (int j = s.j0; j < s.j1; ++j, ++kc) {
-            const int st = kc % C::kStages;
-            const uint32_t par = ((kc / C::kStages) - 1) & 1;
-            const int key = j * kKeys + g * a.box;
-            int page = 0, row = s.k0 + key;
-            bool bad = false;
-            if (!a.cu_k) {
-              page = a.P_pool;   // out of range: zeros
-              row = 0;
-              if (key < s.L) {
-                const int ph = page_at(a.pt, s.b, key / a.P);
-                bad = ph < 0 || ph >= a.P_pool;
-                if (!bad) page = ph, row = key % a.P;
-              }
-            }
-            const uint32_t bits = __ballot_sync(0xffffffffu, bad) & ((1u << nb) - 1u);
-            if (kc >= (uint32_t)C::kStages && !warp_wait(&k_empty[st], par, abort_flag)) {
-              ok = false;
-              break;
-            }
+          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc) {
+            const Box x = box_of(a, s, j, lane);
             if (lane == 0) {
-              bad_s[kc % kBadRing] = bits;
-              if (bits) set_dev_error(a.err, SA_DEVERR_POOL_RANGE);
-              mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
+              bad_s[kc % kBadRing] = x.bad;
+              if (x.bad) set_dev_error(a.err, SA_DEVERR_POOL_RANGE);
             }
-            __syncwarp();
-            if (ch < C::kChunks)
-              tma_load_4d(k_s + st * C::kTileBytes + ch * (kKeys * 128) + g * a.box * 128, &kmap,
-                          &k_full[st], ch * 64, row, s.kvh, page);
-            if (kc >= (uint32_t)C::kStages && !warp_wait(&v_empty[st], par, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
-            __syncwarp();
-            if (ch < C::kChunks)
-              tma_load_4d(v_s + st * C::kTileBytes + ch * (kKeys * 128) + g * a.box * 128, &vmap,
-                          &v_full[st], ch * 64, row, s.kvh, page);
+            ok = load_tile<D>(x, s.kvh, kc, k_s, &kmap, k_full, k_empty, a.box, abort_flag);
           }
         }
         cta_sync();
       }
     } else if (warp == kQWarp) {
-      // ================= queries
+      // ================= queries; value rows past a sequence's end
+      uint32_t tails = 0;
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
         for (int i = 0; i < n_segs && ok; ++i) {
           const Seg& s = seg_s[i];
-          if (s.j0 == s.j1) continue;
+          const int nt = s.j1 - s.j0, j = s.j1 - 1;
+          if (nt == 0) continue;
           if (qc > 0 && !warp_wait(&q_empty, (qc - 1) & 1, abort_flag)) {
             ok = false;
             break;
@@ -537,6 +591,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s.kvh * G, s.q0 + s.r0 / G + w * a.tile_toks, 0);
           }
           ++qc;
+          // the rows may hold anything (0 * NaN): zeroed in the tile, up to the
+          // 16-key step that is multiplied
+          const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
+          const int rows = 16 * min(8, (hi - j * kKeys + 15) / 16), z0 = s.L - j * kKeys;
+          if (z0 < rows) {
+            const uint32_t c = kc + nt - 1;
+            const int st = c % C::kStages;
+            ok = warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag);
+            uint8_t* vt = v_s + st * C::kTileBytes;
+            for (int x = lane; x < (rows - z0) * C::kChunks * 8; x += 32) {
+              const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
+              *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 + (p & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async();
+            // one tail at a time: v_tail has a single phase to wait for
+            if (tails > 0) ok = ok && warp_wait(&v_tail_seen, (tails - 1) & 1, abort_flag);
+            mbar_arrive(&v_tail);
+            ++tails;
+          }
+          kc += nt;
         }
         cta_sync();
       }
@@ -647,9 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         cta_sync();
       }
     } else if (warp == kPlanWarp) {
-      // ================= planner
+      // ================= planner, V tiles
       // ---- this CTA's share [w_lo, w_hi) of all units, and where it starts
       int64_t w_total = 0, w_pos = 0, w_hi = 0;   // w_pos: the next unit to plan
+      int64_t w_share = 0;
+      int w_extra = 0;
       int n_eff = 1, cb = 0, ckvh = 0, cqt = 0;   // the item that holds w_pos
       int64_t c_off = 0;                          // units of that item before w_pos
         int64_t part = 0;
@@ -658,8 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         w_total = part * a.Hkv;
         n_eff = (int)min((int64_t)n_ctas, max((int64_t)1, w_total / kMinUnits));
         if (cta < n_eff) {
-          w_pos = w_total * cta / n_eff;
-          w_hi = w_total * (cta + 1) / n_eff;
+          // shares of w_share or w_share + 1 units, the first w_extra the longer
+          w_share = quot(w_total, n_eff);
+          w_extra = (int)(w_total - w_share * n_eff);
+          w_pos = w_share * cta + min(cta, w_extra);
+          w_hi = w_pos + w_share + (cta < w_extra);
         }
         if (w_pos < w_hi) {
           // the sequence: 32 at a time
@@ -683,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             before += __shfl_sync(0xffffffffu, incl, 31);
           }
           int64_t off = w_pos - before * a.Hkv;
-          ckvh = (int)(off / units_s[cb]);
+          ckvh = (int)quot(off, units_s[cb]);
           off -= (int64_t)ckvh * units_s[cb];
           // the row tile: 32 at a time
           const Seq s = seq_of(a, cb, nullptr);
@@ -706,7 +786,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             off -= __shfl_sync(0xffffffffu, incl, 31);
           }
         }
-      uint32_t tails = 0;
       bool last = false;
       do {
         // the next segments
@@ -734,7 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   g.part = 2 * cta + (ta == 0);
                   if (ta == 0) {   // the parts that follow are the next CTAs' first ones
                     const int64_t e = w_pos - ua + units;   // the item's end
-                    const int last = (int)((e * n_eff + w_total - 1) / w_total) - 1;
+                    const int64_t cut = (w_share + 1) * w_extra;   // the longer shares' end
+                    const int last = (int)(e <= cut ? quot(e - 1, w_share + 1)
+                                                    : w_extra + quot(e - 1 - cut, w_share));
                     int32_t* h = a.part_head + cta * 8;
                     h[0] = g.nr, h[1] = last - cta + 1;
                     h[2] = s.q0, h[3] = g.r0, h[4] = ckvh;
@@ -752,43 +833,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         cta_sync();
-        // value rows past a sequence's end may hold anything (0 * NaN): zeroed in
-        // the tile, up to the 16-key step that is multiplied
         last = last_s;
         const int n_segs = n_segs_s;
-        for (int i = 0; i < n_segs && ok; ++i) {
-          const Seg& s = seg_s[i];
-          const int nt = s.j1 - s.j0, j = s.j1 - 1;
-          const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
-          const int rows = 16 * min(8, (hi - j * kKeys + 15) / 16), z0 = s.L - j * kKeys;
-          if (nt > 0 && z0 < rows) {
-            const uint32_t c = kc + nt - 1;
-            const int st = c % C::kStages;
-            ok = warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag);
-            uint8_t* vt = v_s + st * C::kTileBytes;
-            for (int x = lane; x < (rows - z0) * C::kChunks * 8; x += 32) {
-              const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
-              *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 + (p & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_proxy_async();
-            // one tail at a time: v_tail has a single phase to wait for
-            if (tails > 0) ok = ok && warp_wait(&v_tail_seen, (tails - 1) & 1, abort_flag);
-            mbar_arrive(&v_tail);
-            ++tails;
-          }
-          kc += nt;
+        for (int i = 0; i < n_segs && ok; ++i) {   // V tiles
+          const Seg s = seg_s[i];
+          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc)
+            ok = load_tile<D>(box_of(a, s, j, lane), s.kvh, kc, v_s, &vmap, v_full, v_empty, a.box,
+                              abort_flag);
         }
         cta_sync();
       } while (!last);
     }
   }
-  if (warp == kLoadWarp && abort_s) {
-    // give up only when no copy of this CTA is in flight any more
-    for (uint32_t c = kc > (uint32_t)C::kStages ? kc - C::kStages : 0; c <= kc; ++c) {
-      mbar_wait_bounded(&k_full[c % C::kStages], (c / C::kStages) & 1);
-      if (c < kc) mbar_wait_bounded(&v_full[c % C::kStages], (c / C::kStages) & 1);
-    }
+  if ((warp == kLoadWarp || warp == kPlanWarp) && abort_s) {
+    // leave only when no copy of this CTA is in flight any more (the last wait
+    // of a tile that was never asked for runs out)
+    uint64_t* full = warp == kLoadWarp ? k_full : v_full;
+    for (uint32_t c = kc > (uint32_t)C::kStages ? kc - C::kStages : 0; c < kc; ++c)
+      for (uint32_t n = 0; n < 1u << 16 && !mbar_try_wait(&full[c % C::kStages],
+                                                        (c / C::kStages) & 1); ++n) {}
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -799,51 +862,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of the cut items: block x takes the item that starts in CTA x's share.
-// One warp per row, four columns per lane; part 0 is CTA x's starting part, the
-// others the continuing parts of the CTAs after it.
-template <int D>
-__global__ void __launch_bounds__(256) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
+// A warp does R rows at a time (their loads in flight together), four columns
+// per lane; part 0 is CTA x's starting part, the others the continuing parts of
+// the CTAs after it.
+template <int D, int R>
+__global__ void __launch_bounds__(512) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
+  pdl_wait_and_release();
   const int32_t* h = a.part_head + blockIdx.x * 8;
-  const int nr = h[0];
-  if (nr == 0) return;
-  const int np = h[1], q0 = h[2], r0 = h[3], kvh = h[4];
-  const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int x = blockIdx.x;
-  auto part = [&](int p) { return p == 0 ? 2 * x + 1 : 2 * (x + p); };
-  for (int rr = blockIdx.y * 8 + warp; rr < nr; rr += gridDim.y * 8) {
-    float m = -INFINITY;
-    for (int p = lane; p < np; p += 32)
-      m = fmaxf(m, a.part_lse[(int64_t)part(p) * a.rows_cap + rr]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float tot = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < np && m != -INFINITY; p0 += 32) {
-      const int p = p0 + lane;
-      const float wl =
-          p < np ? exp2f(a.part_lse[(int64_t)part(p) * a.rows_cap + rr] - m) : 0.f;
-      tot += wl;
-      const int cnt = min(32, np - p0);
+  const int nr = h[0], np = h[1], q0 = h[2], row0 = h[3], kvh = h[4];
+  const int lane = threadIdx.x & 31;
+  const int rr = (blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * R;
+  if (rr >= nr) return;
+  const int G = a.Hq / a.Hkv, x = blockIdx.x;
+  auto part_row = [&](int p, int r) {   // row rr + r of part p (rows past the last: the last)
+    return (int64_t)(p == 0 ? 2 * x + 1 : 2 * (x + p)) * a.rows_cap + min(rr + r, nr - 1);
+  };
+  float m[R], tot[R];
+  float4 acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) m[r] = -INFINITY, tot[r] = 0.f, acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = lane; p < np; p += 32)
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = max_nan(m[r], a.part_lse[part_row(p, r)]);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    for (int o = 16; o; o >>= 1) m[r] = max_nan(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
+  for (int p0 = 0; p0 < np; p0 += 32) {
+    float w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[r] = p0 + lane < np && m[r] != -INFINITY
+                 ? exp2f(a.part_lse[part_row(p0 + lane, r)] - m[r]) : 0.f;
+      tot[r] += w[r];
+    }
+    const int cnt = min(32, np - p0);
 #pragma unroll 4
-      for (int i = 0; i < cnt; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wl, i);
+    for (int i = 0; i < cnt; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float wi = __shfl_sync(0xffffffffu, w[r], i);
         if (lane < D / 4) {
-          const float4 v = *reinterpret_cast<const float4*>(
-              a.part_o + ((int64_t)part(p0 + i) * a.rows_cap + rr) * D + lane * 4);
-          acc.x = fmaf(wi, v.x, acc.x);
-          acc.y = fmaf(wi, v.y, acc.y);
-          acc.z = fmaf(wi, v.z, acc.z);
-          acc.w = fmaf(wi, v.w, acc.w);
+          const float4 v = *reinterpret_cast<const float4*>(a.part_o + part_row(p0 + i, r) * D +
+                                                            lane * 4);
+          acc[r].x = fmaf(wi, v.x, acc[r].x);
+          acc[r].y = fmaf(wi, v.y, acc[r].y);
+          acc[r].z = fmaf(wi, v.z, acc[r].z);
+          acc[r].w = fmaf(wi, v.w, acc[r].w);
         }
       }
-    }
-    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    const float inv = m == -INFINITY ? 0.f : 1.f / tot;
-    const int rg = r0 + rr, t = rg / G;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    for (int o = 16; o; o >>= 1) tot[r] += __shfl_xor_sync(0xffffffffu, tot[r], o);
+    if (rr + r >= nr) continue;
+    const float inv = m[r] == -INFINITY ? 0.f : 1.f / tot[r];
+    const int rg = row0 + rr + r, t = rg / G;
     const int64_t orow = (int64_t)(q0 + t) * a.Hq + kvh * G + (rg - t * G);
     if (lane < D / 4)
-      *reinterpret_cast<uint2*>(a.o + orow * D + lane * 4) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (lane == 0 && a.lse) a.lse[orow] = m == -INFINITY ? m : (m + log2f(tot)) * kLn2;
+      *reinterpret_cast<uint2*>(a.o + orow * D + lane * 4) = make_uint2(
+          pack_bf16(acc[r].x * inv, acc[r].y * inv), pack_bf16(acc[r].z * inv, acc[r].w * inv));
+    if (lane == 0 && a.lse) a.lse[orow] = m[r] == -INFINITY ? m[r] : (m[r] + log2f(tot[r])) * kLn2;
   }
 }
 
@@ -859,8 +937,13 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensor
   dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, qmap, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int by = (a.rows_cap + 31) / 32;   // 32 rows per block
-  dense_merge_kernel<D><<<dim3(ctas, by), 256, 0, stream>>>(a);
+  // (few rows: one per warp, in one block per item; many: four per warp)
+  if (a.rows_cap <= 16) {
+    dense_merge_kernel<D, 1><<<ctas, 32 * a.rows_cap, 0, stream>>>(a);
+  } else {
+    const int by = (a.rows_cap + 63) / 64;
+    dense_merge_kernel<D, 4><<<dim3(ctas, by), 512, 0, stream>>>(a);
+  }
   return cudaGetLastError();
 }
 
