@@ -714,8 +714,9 @@ SA_API int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[
  * The result does not depend on timing: the same call gives the same bits on
  * the same kind of device.
  * Supported: D in {64,128}, page_size a multiple of 16, Hq/Hkv <= 128, B <=
- * 4096, total_q * Hq < 2^30, max_pages * page_size < 2^30 (SA_ERR_UNSUPPORTED
- * otherwise).  Two launches (the second merges parts of items that were split
+ * 4096, total_q * Hq < 2^30, max_pages * page_size < 2^30, and (tokens / 2^7 *
+ * Hq/Hkv + B) * Hkv * (longest sequence / 128) below about 2^31
+ * (SA_ERR_UNSUPPORTED otherwise).  Two launches (the second merges parts of items that were split
  * between SMs).
  */
 SA_API size_t sa_dense_attention_workspace_size(int total_q, int Hq, int Hkv, int D);

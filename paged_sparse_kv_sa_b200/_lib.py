@@ -10,6 +10,7 @@ missing; calls raise instead.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -140,7 +141,7 @@ def _ptr(t):
     keep = getattr(_REC, "keep", None)
     if keep is not None:
         keep.append(t)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _call(fn, args, what):
@@ -846,66 +847,70 @@ def sa_append_kv_dir(k_new, v_new, n_new, k_cache, v_cache, page_dir, page_block
 # packed batches: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 of
 # [tokens, heads, D] tensors (cu [B + 1] int32 on the GPU)
 # ---------------------------------------------------------------------------
-def _strides3(t) -> "ctypes.Array":
-    return _c_i64_3(*t.stride())
+# (these calls are short: what is checked per call is read once and cheaply)
+@functools.lru_cache(maxsize=1024)
+def _stride_array(strides) -> "ctypes.Array":
+    return (ctypes.c_int64 * len(strides))(*strides)
 
 
-def _on_current(device):
+def _on_current(device: int):
     """The calls launch on the current device's stream: tensors of another
     device are refused rather than read from there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device < 0 or device != torch.cuda.current_device():
         raise ValueError("tensors must be on the current GPU")
 
 
+def _same_gpu(t, device: int):
+    if t.get_device() != device:
+        raise ValueError("tensors must be on the same GPU")
+
+
 def _packed(t, heads, D, device, what):
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, D):
         raise TypeError(f"{what} must be a bfloat16 tensor [tokens, {heads}, {D}]")
-    if t.device != device:
-        raise ValueError("tensors must be on the same GPU")
-    return t
+    _same_gpu(t, device)
 
 
-def _dense_i32(t, shape, device, what):
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise TypeError(f"{what} must be a contiguous int32 tensor of shape {shape}")
-    if t.device != device:
-        raise ValueError("tensors must be on the same GPU")
-    return t
-
-
-def _dense_out(t, dtype, shape, device, what):
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise TypeError(f"{what} must be a contiguous {dtype} tensor of shape {shape}")
-    if t.device != device:
-        raise ValueError("tensors must be on the same GPU")
-    return t
+def _dense(t, dtype, shape, device, what):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    _same_gpu(t, device)
 
 
 def _cache_pair(k_cache, v_cache, D, device):
-    if (k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 or k_cache.dim() != 4
-            or k_cache.shape != v_cache.shape or k_cache.shape[3] != D):
+    shape = k_cache.shape
+    if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16
+            or len(shape) != 4 or shape != v_cache.shape or shape[3] != D):
         raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    if k_cache.device != device or v_cache.device != device:
-        raise ValueError("tensors must be on the same GPU")
-    return k_cache.shape
+    _same_gpu(k_cache, device), _same_gpu(v_cache, device)
+    return shape
 
 
 def _error_word(dev_error, device):
-    if dev_error is not None and (dev_error.dtype != torch.int32 or dev_error.device != device):
+    if dev_error is not None and (dev_error.dtype is not torch.int32
+                                  or dev_error.get_device() != device):
         raise TypeError("dev_error must be an int32 tensor on the same GPU")
     return _ptr(dev_error)
 
 
+def _batch_of(cu, device, what):
+    """B of the offsets cu [B + 1]"""
+    if cu.dtype is not torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous int32 tensor [B + 1]")
+    _same_gpu(cu, device)
+    return cu.shape[0] - 1
+
+
 def _flat_args(page_table, B, device):
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    _dense_i32(page_table, (B, page_table.shape[1]), device, "page_table")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or \
+            page_table.shape[0] != B or not page_table.is_contiguous():
+        raise TypeError("page_table must be a contiguous int32 tensor [B, max_pages]")
+    _same_gpu(page_table, device)
     return _ptr(page_table), page_table.shape[1]
 
 
 def _dir_args_on(page_dir, page_blocks, block_shift, B, device):
-    if page_dir.device != device or page_blocks.device != device:
-        raise ValueError("tensors must be on the same GPU")
+    _same_gpu(page_dir, device), _same_gpu(page_blocks, device)
     if page_dir.dim() != 2 or page_dir.shape[0] != B:
         raise ValueError("page_dir must be [B, n_dir]")
     return _dir_args(page_dir, page_blocks, block_shift)
@@ -919,27 +924,27 @@ def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
 
 
 def _dense_common(q, cu_q, Hkv, o_out, lse_out, workspace):
-    if q.dim() != 3 or q.dtype != torch.bfloat16:
+    if q.dim() != 3 or q.dtype is not torch.bfloat16:
         raise TypeError("q must be a bfloat16 tensor [tokens, Hq, D]")
-    dev = q.device
+    dev = q.get_device()
     _on_current(dev)
-    total, Hq, D = q.shape
-    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError("cu_q must be [B + 1]")
-    _dense_i32(cu_q, (cu_q.shape[0],), dev, "cu_q")
+    shape = q.shape
+    total, Hq, D = shape
+    B = _batch_of(cu_q, dev, "cu_q")
     if o_out is None:
-        o_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+        o_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
-        _dense_out(o_out, torch.bfloat16, (total, Hq, D), dev, "o_out")
+        _dense(o_out, torch.bfloat16, shape, dev, "o_out")
     if lse_out is None:
-        lse_out = torch.empty((total, Hq), dtype=torch.float32, device=dev)
+        lse_out = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
     else:
-        _dense_out(lse_out, torch.float32, (total, Hq), dev, "lse_out")
+        _dense(lse_out, torch.float32, shape[:2], dev, "lse_out")
     if workspace is None:
-        workspace = dense_attention_workspace(total, Hq, Hkv, D, dev)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        workspace = dense_attention_workspace(total, Hq, Hkv, D, q.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
+            workspace.get_device() != dev:
         raise TypeError("workspace must be a contiguous uint8 tensor on the same GPU")
-    return total, Hq, D, cu_q.shape[0] - 1, o_out, lse_out, workspace
+    return dev, total, Hq, D, B, o_out, lse_out, workspace
 
 
 def _chunk(name, q, k_cache, v_cache, map_args, seq_lens, cu_q, scale, window, o_out, lse_out,
@@ -947,16 +952,16 @@ def _chunk(name, q, k_cache, v_cache, map_args, seq_lens, cu_q, scale, window, o
     lib = load()
     if k_cache.dim() != 4:
         raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, k_cache.shape[1], o_out,
-                                                               lse_out, workspace)
-    dev = q.device
+    dev, total, Hq, D, B, o_out, lse_out, workspace = _dense_common(
+        q, cu_q, k_cache.shape[1], o_out, lse_out, workspace)
     P_pool, Hkv, P, _ = _cache_pair(k_cache, v_cache, D, dev)
-    _dense_i32(seq_lens, (B,), dev, "seq_lens")
+    _dense(seq_lens, torch.int32, (B,), dev, "seq_lens")
     _call(getattr(lib, name),
-          (_ptr(q), _strides3(q), _ptr(cu_q), total, _ptr(k_cache), _strides4(k_cache),
-           _ptr(v_cache), _strides4(v_cache), *map_args(B, dev), _ptr(seq_lens), B, Hq, Hkv, D, P,
-           P_pool, float(scale), int(window), _ptr(o_out), _ptr(lse_out), _ptr(workspace),
-           workspace.numel(), _error_word(dev_error, dev), _stream(stream)), name)
+          (_ptr(q), _stride_array(q.stride()), _ptr(cu_q), total, _ptr(k_cache),
+           _stride_array(k_cache.stride()), _ptr(v_cache), _stride_array(v_cache.stride()),
+           *map_args(B, dev), _ptr(seq_lens), B, Hq, Hkv, D, P, P_pool, scale, window,
+           _ptr(o_out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
+           _error_word(dev_error, dev), _stream(stream)), name)
     return o_out, lse_out
 
 
@@ -991,70 +996,70 @@ def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_ou
     if k.dim() != 3:
         raise TypeError("k must be a bfloat16 tensor [keys, Hkv, D]")
     Hkv = k.shape[1]
-    total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
-                                                               workspace)
-    dev = q.device
+    dev, total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
+                                                                    workspace)
     _packed(k, Hkv, D, dev, "k"), _packed(v, Hkv, D, dev, "v")
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must hold the same tokens")
-    _dense_i32(cu_k, (B + 1,), dev, "cu_k")
+    if _batch_of(cu_k, dev, "cu_k") != B:
+        raise ValueError("cu_q and cu_k must hold the same sequences")
     _call(lib.sa_prompt_attention,
-          (_ptr(q), _strides3(q), _ptr(cu_q), total, _ptr(k), _strides3(k), _ptr(v), _strides3(v),
-           _ptr(cu_k), k.shape[0], B, Hq, Hkv, D, float(scale), int(window), _ptr(o_out),
-           _ptr(lse_out), _ptr(workspace), workspace.numel(), _error_word(dev_error, dev),
-           _stream(stream)), "sa_prompt_attention")
+          (_ptr(q), _stride_array(q.stride()), _ptr(cu_q), total, _ptr(k),
+           _stride_array(k.stride()), _ptr(v), _stride_array(v.stride()), _ptr(cu_k), k.shape[0],
+           B, Hq, Hkv, D, scale, window, _ptr(o_out), _ptr(lse_out), _ptr(workspace),
+           workspace.numel(), _error_word(dev_error, dev), _stream(stream)),
+          "sa_prompt_attention")
     return o_out, lse_out
 
 
 def _append_rope(name, q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, map_args,
                  seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream):
     lib = load()
-    if k_new.dim() != 3 or k_new.dtype != torch.bfloat16:
+    if k_new.dim() != 3 or k_new.dtype is not torch.bfloat16:
         raise TypeError("k_new must be a bfloat16 tensor [tokens, Hkv, D]")
-    dev = k_new.device
+    dev = k_new.get_device()
     _on_current(dev)
     total, Hkv, D = k_new.shape
     _packed(v_new, Hkv, D, dev, "v_new")
     if v_new.shape[0] != total:
         raise ValueError("k_new and v_new must hold the same tokens")
-    if cu_new.dim() != 1 or cu_new.shape[0] < 1:
-        raise ValueError("cu_new must be [B + 1]")
-    B = cu_new.shape[0] - 1
-    _dense_i32(cu_new, (B + 1,), dev, "cu_new")
-    _dense_i32(seq_lens, (B,), dev, "seq_lens")
+    B = _batch_of(cu_new, dev, "cu_new")
+    _dense(seq_lens, torch.int32, (B,), dev, "seq_lens")
     P_pool, heads, P, _ = _cache_pair(k_cache, v_cache, D, dev)
     if heads != Hkv:
         raise ValueError("the caches must have k_new's heads")
     n_pos = rot = 0
     if rope_table is not None:
-        if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
-                not rope_table.is_contiguous() or rope_table.device != dev:
+        if rope_table.dtype is not torch.float32 or rope_table.dim() != 2 or \
+                not rope_table.is_contiguous():
             raise TypeError("rope_table must be a contiguous float32 tensor [positions, rot_dim]")
+        _same_gpu(rope_table, dev)
         n_pos, rot = rope_table.shape
     Hq = 0
-    qs = _c_i64_3(0, 0, 1)
+    qs = (0, 0, 1)
     if q_new is not None:
         if q_new.dim() != 3 or q_new.shape[0] != total:
             raise ValueError("q_new must hold k_new's tokens")
         Hq = q_new.shape[1]
         _packed(q_new, Hq, D, dev, "q_new")
-        qs = _strides3(q_new)
+        qs = q_new.stride()
         if q_out is None:
-            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q_new.device)
         else:
-            _dense_out(q_out, torch.bfloat16, (total, Hq, D), dev, "q_out")
+            _dense(q_out, torch.bfloat16, (total, Hq, D), dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q_new")
     if k_out is not None:
-        _dense_out(k_out, torch.bfloat16, (total, Hkv, D), dev, "k_out")
+        _dense(k_out, torch.bfloat16, (total, Hkv, D), dev, "k_out")
     if summaries is not None:
-        _dense_out(summaries, torch.bfloat16, (P_pool, Hkv, D), dev, "summaries")
+        _dense(summaries, torch.bfloat16, (P_pool, Hkv, D), dev, "summaries")
     if out_seq_lens is not None:
-        _dense_i32(out_seq_lens, (B,), dev, "out_seq_lens")
+        _dense(out_seq_lens, torch.int32, (B,), dev, "out_seq_lens")
     _call(getattr(lib, name),
-          (_ptr(q_new), qs, _ptr(k_new), _strides3(k_new), _ptr(v_new), _strides3(v_new),
-           _ptr(cu_new), total, _ptr(rope_table), n_pos, rot, int(bool(interleaved)), _ptr(q_out),
-           _ptr(k_out), _ptr(k_cache), _strides4(k_cache), _ptr(v_cache), _strides4(v_cache),
+          (_ptr(q_new), _stride_array(qs), _ptr(k_new), _stride_array(k_new.stride()),
+           _ptr(v_new), _stride_array(v_new.stride()), _ptr(cu_new), total, _ptr(rope_table),
+           n_pos, rot, 1 if interleaved else 0, _ptr(q_out), _ptr(k_out), _ptr(k_cache),
+           _stride_array(k_cache.stride()), _ptr(v_cache), _stride_array(v_cache.stride()),
            *map_args(B, dev), _ptr(seq_lens), _ptr(out_seq_lens), B, Hq, Hkv, D, P, P_pool,
            _ptr(summaries), _error_word(dev_error, dev), _stream(stream)), name)
     return q_out, out_seq_lens

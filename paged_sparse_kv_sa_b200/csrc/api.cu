@@ -1239,6 +1239,15 @@ int rope_append_impl(const uint16_t* q, const int64_t* qs, const uint16_t* k, co
   return cuda_status(launch_rope_append(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Whether the work of a dense attention call, in key tiles, stays below 2^31 for
+// every batch its sizes allow (the kernel lays it out in 32 bits).
+bool dense_countable(const DenseArgs& a, int64_t max_len) {
+  const int64_t toks = 2 * a.tile_toks;
+  const int64_t keys = a.window && a.window + toks < max_len ? a.window + toks : max_len;
+  const int64_t items = a.total_q / toks + a.B;
+  return items * (keys / 128 + 3) < 0x7fffffffLL / a.Hkv;
+}
+
 // What the dense attention calls share: sizes, outputs, workspace.
 int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int total_q, int B,
                  int Hq, int Hkv, int D, float scale, int window, uint16_t* o, float* lse,
@@ -1297,6 +1306,7 @@ int chunk_impl(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int to
   a.seq_lens = seq_lens;
   a.P = page_size;
   a.P_pool = P_pool;
+  if (!dense_countable(a, (int64_t)max_pages * page_size)) return SA_ERR_UNSUPPORTED;
   a.box = 16;
   while (a.box < 128 && page_size % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap qmap, kmap, vmap;
@@ -1400,6 +1410,7 @@ int sa_prompt_attention(const uint16_t* q, const int64_t q_strides[3], const int
     if (total_k > 0x3fffffff || !map_strides(k_strides, 2) || !map_strides(v_strides, 2))
       return SA_ERR_UNSUPPORTED;
   }
+  if (!dense_countable(a, total_k)) return SA_ERR_UNSUPPORTED;
   a.cu_k = cu_k;
   a.total_k = total_k;
   a.P = 128;

@@ -106,11 +106,6 @@ SA_DEV int2 tiles_of(const Seq& s, int toks, int window, int qt) {
   if (hi <= lo) return make_int2(0, 0);
   return make_int2(lo / kKeys, (hi + kKeys - 1) / kKeys);
 }
-// a / b, in 32 bits where both fit.
-SA_DEV int64_t quot(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
 SA_DEV int item_units(const Seq& s, int toks, int window, int qt) {
   const int2 t = tiles_of(s, toks, window, qt);
   return kItemUnits + t.y - t.x;
@@ -126,33 +121,38 @@ struct Seg {
 };
 
 // ---------------------------------------------------------------- waits
-constexpr uint64_t kPatience = 1000000000ull;   // ns; no copy or product takes near as long
-SA_DEV uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
+// Wait for phase `parity`, at most kPolls polls (each suspends the thread for up
+// to microseconds: a second or so in all; no copy or product takes near as long).
+// false: gave up.  The result is meant to be kept and looked at once a tile, not
+// branched on here: a vote or a branch at every wait made the tensor core's
+// issuing warp, and with it every tile, slower (8192-token prompt 535 -> 516 us,
+// packed short prompts 244 -> 213 us without).
+constexpr uint32_t kPolls = 1u << 17;
+SA_DEV bool wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " @p bra D;\n add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra W;\n"
+      "D:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kPolls)
+      : "memory");
+  return ok != 0;
 }
-// Wait for phase `parity`; gives up after kPatience, or when another role has.
-SA_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0 && (*abort_flag || now_ns() - t0 > kPatience)) break;
-  }
+// Whether no lane of the warp has given up; a warp that has raises the CTA's flag,
+// and every warp that sees it goes on without waiting.
+SA_DEV bool all_well(bool ok, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, ok)) return true;
   *abort_flag = 1;
   return false;
-}
-// The same by a whole warp, which goes on together or not at all.
-SA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
 }
 // All threads of the CTA, from whichever role's code they are in.
 SA_DEV void cta_sync() { asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory"); }
 // Registers per thread after the roles part: the launch's 384 x 168 divided as
-// 256 x 208 for the softmax warps (a row of scores is 128 registers) + 128 x 88.
-SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// 256 x 200 for the softmax warps (a row of scores is 128 registers) + 128 x 104.
+SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 // A value every lane holds alike, as the compiler can see.
 template <typename T>
 SA_DEV T uni(T x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -213,7 +213,7 @@ SA_DEV bool load_tile(const Box& x, int kvh, uint32_t c, uint8_t* ring, const CU
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31, nb = kKeys / box, st = c % C::kStages;
   if (c >= (uint32_t)C::kStages &&
-      !warp_wait(&empty[st], ((c / C::kStages) - 1) & 1, abort_flag))
+      !all_well(wait(&empty[st], ((c / C::kStages) - 1) & 1) && !*abort_flag, abort_flag))
     return false;
   if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTileBytes);
   __syncwarp();
@@ -230,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
+  // the merge kernel may be set up under this one's tail: it waits for the end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, n_ctas = gridDim.x;
   const int G = a.Hq / a.Hkv;
@@ -337,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < n_w; ++it, ++cw0) {
           const int ti = halves ? 2 * it + w : it;
           const int k0 = (s.j0 + ti) * kKeys;
-          ok = ok && warp_wait(&s_full[w], cw0 & 1, abort_flag);
-          if (!ok) break;
+          if (!all_well(ok, abort_flag)) break;
+          ok = wait(&s_full[w], cw0 & 1);
           if (!warp_ok) {   // no rows here: whatever P holds reaches no row that is kept
             __syncwarp();
             if (lane == 0) {
@@ -427,14 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- epilogue
         if (n_w > 0) {
-          ok = ok && warp_wait(&o_done[w], oc0 & 1, abort_flag);
+          ok = ok && wait(&o_done[w], oc0 & 1);
           ++oc0;
         }
         float wa = 1.f, wb = 0.f, m_all = m_ref, l_all = l;
         const int id = 1 + quarter;
         if (halves) {   // the other half's running max and sum, and its accumulator
           if (n_other > 0) {
-            ok = ok && warp_wait(&o_done[1 - w], oc1 & 1, abort_flag);
+            ok = ok && wait(&o_done[1 - w], oc1 & 1);
             ++oc1;
           }
           ml_s[w][row] = make_float2(m_ref, l);
@@ -447,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           if (nt > 0) ++oc1;
         }
+        ok = all_well(ok, abort_flag);
         tc::fence_after_sync();
         const bool empty = !ok || l_all == 0.f;
         const float inv = empty ? 0.f : 1.f / l_all;
@@ -576,10 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Seg& s = seg_s[i];
           const int nt = s.j1 - s.j0, j = s.j1 - 1;
           if (nt == 0) continue;
-          if (qc > 0 && !warp_wait(&q_empty, (qc - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = all_well((qc == 0 || wait(&q_empty, (qc - 1) & 1)) && !*abort_flag, abort_flag);
+          if (!ok) break;
           // one box per tile and 64-column chunk; rows of other sequences' tokens
           // that a box holds are never kept, tokens past the tensor load as zeros
           const int tiles = s.nr > tile_rows ? 2 : 1;
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (z0 < rows) {
             const uint32_t c = kc + nt - 1;
             const int st = c % C::kStages;
-            ok = warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag);
+            ok = wait(&v_full[st], (c / C::kStages) & 1);
             uint8_t* vt = v_s + st * C::kTileBytes;
             for (int x = lane; x < (rows - z0) * C::kChunks * 8; x += 32) {
               const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
@@ -607,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_proxy_async();
             // one tail at a time: v_tail has a single phase to wait for
-            if (tails > 0) ok = ok && warp_wait(&v_tail_seen, (tails - 1) & 1, abort_flag);
+            if (tails > 0) ok = wait(&v_tail_seen, (tails - 1) & 1) && ok;
+            ok = all_well(ok, abort_flag);
             mbar_arrive(&v_tail);
             ++tails;
           }
@@ -624,168 +626,155 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v_desc = uni(tc::desc_lo(smem_u32(v_s), kKeys * 128));
       const uint32_t tmem_u = uni(tmem);
       uint32_t tails = 0;
+      // One run of an item's tiles.  halves: each row tile has every other key tile.
+      auto run = [&](int j0, int nt, int L, int hi, auto hv) {
+        constexpr bool halves = decltype(hv)::value != 0;
+        const int n_a = halves ? (nt + 1) / 2 : nt, n_b = halves ? nt / 2 : nt;
+        int qk_left = n_a + n_b;
+        // S_w = Q_w K^T of the tile of iteration it
+        auto qk = [&](int it, auto wc) {
+          constexpr int w = decltype(wc)::value;
+          const uint32_t c = kc + (halves ? 2 * it + w : it);
+          const int st = c % C::kStages;
+          if (halves || w == 0) {
+            ok = wait(&k_full[st], (c / C::kStages) & 1) && ok;
+            tc::fence_after_sync();
+          }
+          if (tc::elect_one()) {
+            const uint32_t qd = q_desc + ((halves ? 0 : w) * C::kQBytes >> 4);
+            const uint32_t kd = k_desc + st * (C::kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4;
+              tc::mma_bf16_lo(tmem_u + 128 * w, qd + o, kd + o, C::kIdQK, kk > 0 ? 1u : 0u);
+            }
+            tc::commit(&s_full[w]);
+            if (halves || w == 1) tc::commit(&k_empty[st]);
+            if (qk_left == 1) tc::commit(&q_empty);
+          }
+          __syncwarp();
+          --qk_left;
+        };
+        // O_w += P_w V of the tile of iteration it
+        auto pv = [&](int it, auto wc) {
+          constexpr int w = decltype(wc)::value;
+          const int ti = halves ? 2 * it + w : it;
+          const uint32_t c = kc + ti;
+          const int st = c % C::kStages, j = j0 + ti;
+          // 16-key steps some row of the item sees
+          const int steps = min(8, (hi - j * kKeys + 15) / 16);
+          const uint32_t vd = v_desc + st * (C::kTileBytes >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = wait(&p_full[w][h], (w ? cw1 : cw0) & 1) && ok;
+            if (h == 0 && (halves || w == 0)) {
+              ok = wait(&v_full[st], (c / C::kStages) & 1) && ok;
+              if (L - j * kKeys < 16 * steps) {   // rows past the end: zeroed first
+                ok = wait(&v_tail, tails & 1) && ok;
+                if (lane == 0) mbar_arrive(&v_tail_seen);
+                ++tails;
+              }
+            }
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                if (kk < steps)
+                  tc::mma_bf16_ts_lo(tmem_u + 256 + D * w, tmem_u + 128 * w + 8 * kk,
+                                     vd + kk * (2048 >> 4), C::kIdPV,
+                                     (it > 0 || kk > 0) ? 1u : 0u);
+              if (h == 1) {
+                if (halves || w == 1) tc::commit(&v_empty[st]);
+                if (it + 1 == (w ? n_b : n_a)) tc::commit(&o_done[w]);
+              }
+            }
+            __syncwarp();
+          }
+          w ? ++cw1 : ++cw0;
+        };
+        ok = wait(&q_full, qc & 1) && ok;
+        tc::fence_after_sync();
+        qk(0, A);
+        if (n_b > 0) qk(0, B);
+        for (int it = 0; it < n_a && all_well(ok, abort_flag); ++it) {
+          pv(it, A);
+          if (it + 1 < n_a) qk(it + 1, A);
+          if (it >= n_b) continue;
+          pv(it, B);
+          if (it + 1 < n_b) qk(it + 1, B);
+        }
+      };
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
-        {
-          for (int i = 0; i < n_segs && ok; ++i) {
-            const Seg& s = seg_s[i];
-            const int j0 = uni(s.j0), nt = uni(s.j1) - j0, L = uni(s.L), nr = uni(s.nr);
-            if (nt == 0) continue;
-            const bool halves = nr <= tile_rows;
-            const int n_a = halves ? (nt + 1) / 2 : nt, n_b = halves ? nt / 2 : nt;
-            int qk_left = n_a + n_b;
-            const int hi = uni(min(L, L - s.n + (s.r0 + nr - 1) / G + 1));
-            auto qk = [&](int it, auto wc) {
-              constexpr int w = decltype(wc)::value;
-              const uint32_t c = kc + (halves ? 2 * it + w : it);
-              const int st = c % C::kStages;
-              if (halves || w == 0) {
-                if (!warp_wait(&k_full[st], (c / C::kStages) & 1, abort_flag)) return false;
-                tc::fence_after_sync();
-              }
-              if (tc::elect_one()) {
-                const uint32_t qd = q_desc + ((halves ? 0 : w) * C::kQBytes >> 4);
-                const uint32_t kd = k_desc + st * (C::kTileBytes >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t o = ((kk >> 2) * (kM * 128) + (kk & 3) * 32) >> 4;
-                  tc::mma_bf16_lo(tmem_u + 128 * w, qd + o, kd + o, C::kIdQK, kk > 0 ? 1u : 0u);
-                }
-                tc::commit(&s_full[w]);
-                if (halves || w == 1) tc::commit(&k_empty[st]);
-                if (qk_left == 1) tc::commit(&q_empty);
-              }
-              __syncwarp();
-              --qk_left;
-              return true;
-            };
-            auto pv = [&](int it, auto wc) {
-              constexpr int w = decltype(wc)::value;
-              const int ti = halves ? 2 * it + w : it;
-              const uint32_t c = kc + ti;
-              const int st = c % C::kStages, j = j0 + ti;
-              // 16-key steps some row of the item sees
-              const int steps = min(8, (hi - j * kKeys + 15) / 16);
-              const uint32_t vd = v_desc + st * (C::kTileBytes >> 4);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (!warp_wait(&p_full[w][h], (w ? cw1 : cw0) & 1, abort_flag)) return false;
-                if (h == 0 && (halves || w == 0)) {
-                  if (!warp_wait(&v_full[st], (c / C::kStages) & 1, abort_flag)) return false;
-                  if (L - j * kKeys < 16 * steps) {   // rows past the end: zeroed first
-                    if (!warp_wait(&v_tail, tails & 1, abort_flag)) return false;
-                    if (lane == 0) mbar_arrive(&v_tail_seen);
-                    ++tails;
-                  }
-                }
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-#pragma unroll
-                  for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                    if (kk < steps)
-                      tc::mma_bf16_ts_lo(tmem_u + 256 + D * w, tmem_u + 128 * w + 8 * kk,
-                                         vd + kk * (2048 >> 4), C::kIdPV,
-                                         (it > 0 || kk > 0) ? 1u : 0u);
-                }
-                __syncwarp();
-              }
-              w ? ++cw1 : ++cw0;
-              if ((halves || w == 1) && tc::elect_one()) tc::commit(&v_empty[st]);
-              __syncwarp();
-              return true;
-            };
-            ok = warp_wait(&q_full, qc & 1, abort_flag);
-            tc::fence_after_sync();
-            ok = ok && qk(0, A) && (n_b == 0 || qk(0, B));
-            for (int it = 0; ok && it < n_a; ++it) {
-              ok = pv(it, A);
-              if (ok && it + 1 < n_a)
-                ok = qk(it + 1, A);
-              else if (tc::elect_one())
-                tc::commit(&o_done[0]);
-              __syncwarp();
-              if (!ok || it >= n_b) continue;
-              ok = pv(it, B);
-              if (ok && it + 1 < n_b)
-                ok = qk(it + 1, B);
-              else if (tc::elect_one())
-                tc::commit(&o_done[1]);
-              __syncwarp();
-            }
-            kc += nt;
-            ++qc;
-          }
+        for (int i = 0; i < n_segs && all_well(ok, abort_flag); ++i) {
+          const Seg& s = seg_s[i];
+          const int j0 = uni(s.j0), nt = uni(s.j1) - j0, L = uni(s.L), nr = uni(s.nr);
+          if (nt == 0) continue;
+          const int hi = uni(min(L, L - s.n + (s.r0 + nr - 1) / G + 1));
+          if (nr <= tile_rows)
+            run(j0, nt, L, hi, B);
+          else
+            run(j0, nt, L, hi, A);
+          kc += nt;
+          ++qc;
         }
-        __syncwarp();
         cta_sync();
       }
     } else if (warp == kPlanWarp) {
       // ================= planner, V tiles
-      // ---- this CTA's share [w_lo, w_hi) of all units, and where it starts
-      int64_t w_total = 0, w_pos = 0, w_hi = 0;   // w_pos: the next unit to plan
-      int64_t w_share = 0;
-      int w_extra = 0;
-      int n_eff = 1, cb = 0, ckvh = 0, cqt = 0;   // the item that holds w_pos
-      int64_t c_off = 0;                          // units of that item before w_pos
-        int64_t part = 0;
-        for (int b = lane; b < a.B; b += 32) part += units_s[b];
-        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-        w_total = part * a.Hkv;
-        n_eff = (int)min((int64_t)n_ctas, max((int64_t)1, w_total / kMinUnits));
-        if (cta < n_eff) {
-          // shares of w_share or w_share + 1 units, the first w_extra the longer
-          w_share = quot(w_total, n_eff);
-          w_extra = (int)(w_total - w_share * n_eff);
-          w_pos = w_share * cta + min(cta, w_extra);
-          w_hi = w_pos + w_share + (cta < w_extra);
+      // ---- this CTA's share [w_pos, w_hi) of all units (fewer than 2^31: checked on
+      // the host), and the item it starts in.  Shares of w_share or w_share + 1
+      // units, the first w_extra of them the longer.
+      int w_total = 0;
+      for (int b = lane; b < a.B; b += 32) w_total += units_s[b];
+      w_total = __reduce_add_sync(0xffffffffu, w_total) * a.Hkv;
+      const int n_eff = min(n_ctas, max(1, w_total / kMinUnits));
+      const int w_share = w_total / n_eff, w_extra = w_total - w_share * n_eff;
+      int w_pos = w_share * cta + min(cta, w_extra);
+      const int w_hi = cta < n_eff ? w_pos + w_share + (cta < w_extra) : w_pos;
+      int cb = 0, ckvh = 0, cqt = 0, c_off = 0;   // c_off: units of the item before w_pos
+      auto scan = [&](int x) {   // inclusive, over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
         }
-        if (w_pos < w_hi) {
-          // the sequence: 32 at a time
-          int64_t before = 0;
-          for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int b = b0 + lane;
-            int64_t incl = b < a.B ? units_s[b] : 0;
-            for (int o = 1; o < 32; o <<= 1) {
-              const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-              if (lane >= o) incl += y;
-            }
-            const uint32_t m =
-                __ballot_sync(0xffffffffu, b < a.B && (before + incl) * a.Hkv > w_pos);
-            if (m) {
-              const int src = __ffs(m) - 1;
-              cb = b0 + src;
-              const int64_t i = __shfl_sync(0xffffffffu, incl, src);
-              before += i - units_s[cb];
-              break;
-            }
-            before += __shfl_sync(0xffffffffu, incl, 31);
+        return x;
+      };
+      if (w_pos < w_hi) {
+        int off = w_pos;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {   // the sequence, 32 at a time
+          const int b = b0 + lane;
+          const int own = b < a.B ? units_s[b] * a.Hkv : 0, incl = scan(own);
+          const uint32_t m = __ballot_sync(0xffffffffu, incl > off);
+          if (m) {
+            const int src = __ffs(m) - 1;
+            cb = b0 + src;
+            off -= __shfl_sync(0xffffffffu, incl - own, src);
+            break;
           }
-          int64_t off = w_pos - before * a.Hkv;
-          ckvh = (int)quot(off, units_s[cb]);
-          off -= (int64_t)ckvh * units_s[cb];
-          // the row tile: 32 at a time
-          const Seq s = seq_of(a, cb, nullptr);
-          const int nqt = (s.n + toks - 1) / toks;
-          for (int q0 = 0; q0 < nqt; q0 += 32) {
-            const int qt = q0 + lane;
-            int incl = qt < nqt ? item_units(s, toks, a.window, qt) : 0;
-            const int own = incl;
-            for (int o = 1; o < 32; o <<= 1) {
-              const int y = __shfl_up_sync(0xffffffffu, incl, o);
-              if (lane >= o) incl += y;
-            }
-            const uint32_t m = __ballot_sync(0xffffffffu, qt < nqt && incl > off);
-            if (m) {
-              const int src = __ffs(m) - 1;
-              cqt = q0 + src;
-              c_off = off - __shfl_sync(0xffffffffu, incl - own, src);
-              break;
-            }
-            off -= __shfl_sync(0xffffffffu, incl, 31);
-          }
+          off -= __shfl_sync(0xffffffffu, incl, 31);
         }
+        const int per_head = units_s[cb];
+        ckvh = off / per_head;
+        off -= ckvh * per_head;
+        const Seq s = seq_of(a, cb, nullptr);
+        const int nqt = (s.n + toks - 1) / toks;
+        for (int q0 = 0; q0 < nqt; q0 += 32) {   // the row tile, 32 at a time
+          const int qt = q0 + lane;
+          const int own = qt < nqt ? item_units(s, toks, a.window, qt) : 0, incl = scan(own);
+          const uint32_t m = __ballot_sync(0xffffffffu, incl > off);
+          if (m) {
+            const int src = __ffs(m) - 1;
+            cqt = q0 + src;
+            c_off = off - __shfl_sync(0xffffffffu, incl - own, src);
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
       bool last = false;
       do {
         // the next segments
@@ -797,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (w_pos < w_hi && ns < kMaxSegs && ckvh < a.Hkv && nqt > 0) {
               const int2 t = tiles_of(s, toks, a.window, cqt);
               const int nt = t.y - t.x, units = kItemUnits + nt;
-              const int ua = (int)c_off;
-              const int ub = (int)min((int64_t)units, c_off + (w_hi - w_pos));
+              const int ua = c_off, ub = min(units, c_off + (w_hi - w_pos));
               // units past the item's fixed cost are its tiles
               const int ta = max(0, ua - kItemUnits), tb = max(0, ub - kItemUnits);
               if (tb > ta || nt == 0) {
@@ -812,10 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ta > 0 || tb < nt) {
                   g.part = 2 * cta + (ta == 0);
                   if (ta == 0) {   // the parts that follow are the next CTAs' first ones
-                    const int64_t e = w_pos - ua + units;   // the item's end
-                    const int64_t cut = (w_share + 1) * w_extra;   // the longer shares' end
-                    const int last = (int)(e <= cut ? quot(e - 1, w_share + 1)
-                                                    : w_extra + quot(e - 1 - cut, w_share));
+                    const int e = w_pos - ua + units - 1;         // the item's last unit
+                    const int cut = (w_share + 1) * w_extra;      // the longer shares' end
+                    const int last =
+                        e < cut ? e / (w_share + 1) : w_extra + (e - cut) / w_share;
                     int32_t* h = a.part_head + cta * 8;
                     h[0] = g.nr, h[1] = last - cta + 1;
                     h[2] = s.q0, h[3] = g.r0, h[4] = ckvh;
@@ -862,66 +850,82 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of the cut items: block x takes the item that starts in CTA x's share.
-// A warp does R rows at a time (their loads in flight together), four columns
-// per lane; part 0 is CTA x's starting part, the others the continuing parts of
-// the CTAs after it.
+// A warp does R rows at a time, four columns per lane; part 0 is CTA x's starting
+// part, the others the continuing parts of the CTAs after it.  Most cut items have
+// two parts: both parts' loads of all rows are in flight together.
 template <int D, int R>
-__global__ void __launch_bounds__(512) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
+__global__ void __launch_bounds__(1024) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
   pdl_wait_and_release();
   const int32_t* h = a.part_head + blockIdx.x * 8;
-  const int nr = h[0], np = h[1], q0 = h[2], row0 = h[3], kvh = h[4];
+  const int4 h0 = *reinterpret_cast<const int4*>(h);
+  const int nr = h0.x, np = h0.y, q0 = h0.z, row0 = h0.w, kvh = h[4];
   const int lane = threadIdx.x & 31;
   const int rr = (blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * R;
   if (rr >= nr) return;
   const int G = a.Hq / a.Hkv, x = blockIdx.x;
-  auto part_row = [&](int p, int r) {   // row rr + r of part p (rows past the last: the last)
-    return (int64_t)(p == 0 ? 2 * x + 1 : 2 * (x + p)) * a.rows_cap + min(rr + r, nr - 1);
+  // row rr + r of part p (rows past the last: the last); fewer than 2^31 rows in all
+  auto part_row = [&](int p, int r) {
+    return (p == 0 ? 2 * x + 1 : 2 * (x + p)) * a.rows_cap + min(rr + r, nr - 1);
   };
-  float m[R], tot[R];
-  float4 acc[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) m[r] = -INFINITY, tot[r] = 0.f, acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = lane; p < np; p += 32)
-#pragma unroll
-    for (int r = 0; r < R; ++r) m[r] = max_nan(m[r], a.part_lse[part_row(p, r)]);
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    for (int o = 16; o; o >>= 1) m[r] = max_nan(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
-  for (int p0 = 0; p0 < np; p0 += 32) {
-    float w[R];
+  auto load = [&](int row) {
+    return lane < D / 4 ? *reinterpret_cast<const float4*>(a.part_o + (int64_t)row * D + lane * 4)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto finish = [&](int r, float4 v, float m, float tot) {   // v: sum of 2^(lse - m) o
+    if (rr + r >= nr) return;
+    const float inv = m == -INFINITY ? 0.f : 1.f / tot;
+    const int rg = row0 + rr + r, t = rg / G;
+    const int orow = (q0 + t) * a.Hq + kvh * G + (rg - t * G);
+    if (lane < D / 4)
+      *reinterpret_cast<uint2*>(a.o + (int64_t)orow * D + lane * 4) = make_uint2(
+          pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    if (lane == 0 && a.lse) a.lse[orow] = m == -INFINITY ? m : (m + log2f(tot)) * kLn2;
+  };
+  if (np == 2) {
+    float l0[R], l1[R];
+    float4 o0[R], o1[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      w[r] = p0 + lane < np && m[r] != -INFINITY
-                 ? exp2f(a.part_lse[part_row(p0 + lane, r)] - m[r]) : 0.f;
-      tot[r] += w[r];
+      l0[r] = a.part_lse[part_row(0, r)];
+      l1[r] = a.part_lse[part_row(1, r)];
+      o0[r] = load(part_row(0, r));
+      o1[r] = load(part_row(1, r));
     }
-    const int cnt = min(32, np - p0);
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float wi = __shfl_sync(0xffffffffu, w[r], i);
-        if (lane < D / 4) {
-          const float4 v = *reinterpret_cast<const float4*>(a.part_o + part_row(p0 + i, r) * D +
-                                                            lane * 4);
-          acc[r].x = fmaf(wi, v.x, acc[r].x);
-          acc[r].y = fmaf(wi, v.y, acc[r].y);
-          acc[r].z = fmaf(wi, v.z, acc[r].z);
-          acc[r].w = fmaf(wi, v.w, acc[r].w);
-        }
-      }
+    for (int r = 0; r < R; ++r) {
+      const float m = max_nan(l0[r], l1[r]);
+      const float w0 = m == -INFINITY ? 0.f : exp2f(l0[r] - m);
+      const float w1 = m == -INFINITY ? 0.f : exp2f(l1[r] - m);
+      finish(r,
+             make_float4(fmaf(w0, o0[r].x, w1 * o1[r].x), fmaf(w0, o0[r].y, w1 * o1[r].y),
+                         fmaf(w0, o0[r].z, w1 * o1[r].z), fmaf(w0, o0[r].w, w1 * o1[r].w)),
+             m, w0 + w1);
+    }
+    return;
   }
-#pragma unroll
+#pragma unroll 1
   for (int r = 0; r < R; ++r) {
-    for (int o = 16; o; o >>= 1) tot[r] += __shfl_xor_sync(0xffffffffu, tot[r], o);
-    if (rr + r >= nr) continue;
-    const float inv = m[r] == -INFINITY ? 0.f : 1.f / tot[r];
-    const int rg = row0 + rr + r, t = rg / G;
-    const int64_t orow = (int64_t)(q0 + t) * a.Hq + kvh * G + (rg - t * G);
-    if (lane < D / 4)
-      *reinterpret_cast<uint2*>(a.o + orow * D + lane * 4) = make_uint2(
-          pack_bf16(acc[r].x * inv, acc[r].y * inv), pack_bf16(acc[r].z * inv, acc[r].w * inv));
-    if (lane == 0 && a.lse) a.lse[orow] = m[r] == -INFINITY ? m[r] : (m[r] + log2f(tot[r])) * kLn2;
+    float m = -INFINITY, tot = 0.f;
+    for (int p = lane; p < np; p += 32) m = max_nan(m, a.part_lse[part_row(p, r)]);
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < np; p0 += 32) {
+      const int p = p0 + lane;
+      const float w = p < np && m != -INFINITY ? exp2f(a.part_lse[part_row(p, r)] - m) : 0.f;
+      tot += w;
+      const int cnt = min(32, np - p0);
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float4 v = load(part_row(p0 + i, r));
+        acc.x = fmaf(wi, v.x, acc.x);
+        acc.y = fmaf(wi, v.y, acc.y);
+        acc.z = fmaf(wi, v.z, acc.z);
+        acc.w = fmaf(wi, v.w, acc.w);
+      }
+    }
+    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    finish(r, acc, m, tot);
   }
 }
 
@@ -937,14 +941,23 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensor
   dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, qmap, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // (few rows: one per warp, in one block per item; many: four per warp)
+  // the merge is launched under the first kernel's tail (it waits for its end);
+  // few rows: one per warp, in one block per item; many: four per warp
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
   if (a.rows_cap <= 16) {
-    dense_merge_kernel<D, 1><<<ctas, 32 * a.rows_cap, 0, stream>>>(a);
-  } else {
-    const int by = (a.rows_cap + 63) / 64;
-    dense_merge_kernel<D, 4><<<dim3(ctas, by), 512, 0, stream>>>(a);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * a.rows_cap);
+    return cudaLaunchKernelEx(&cfg, dense_merge_kernel<D, 1>, a);
   }
-  return cudaGetLastError();
+  cfg.gridDim = dim3(ctas, (a.rows_cap + 127) / 128);
+  cfg.blockDim = dim3(1024);
+  return cudaLaunchKernelEx(&cfg, dense_merge_kernel<D, 4>, a);
 }
 
 int rows_cap_of(int total_q, int Hq, int Hkv) {

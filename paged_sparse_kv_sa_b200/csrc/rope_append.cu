@@ -12,11 +12,14 @@
 // result one rounding to bf16: the stored bits are those of the plain formula.
 //
 // Two kinds of CTA share the launch.  A page CTA owns one (touched page, kv
-// head): its threads own fixed columns (16-byte pieces, both halves of a
-// rotated pair) and stride over the page's rows, so each reads the old keys or
-// the new ones, rotates, writes, and sums its columns in float64 on the way;
-// the row groups' sums meet in shared memory.  A query CTA rotates the heads of
-// a few tokens.  Page slots and tokens find their sequence by a 32-way search
+// head): it reads the page's old keys and rotates and writes the new ones in
+// 16-byte pieces (both halves of a rotated pair in one thread), leaves them in
+// shared memory as well, and then sums each column in float64 from there (one
+// column per thread: few registers, so enough CTAs are resident to keep the
+// loads in flight; the sums kept per thread while loading took 109 us where
+// this takes 43 us for 8254 tokens).  A query CTA rotates the heads of a few
+// tokens, one warp per token: a lane keeps its unit of the head, so it reads its
+// cosines and sines once for all heads.  Page slots and tokens find their sequence by a 32-way search
 // of the offsets: slot s belongs to the last b with floor(cu[b]/P) + 2b <= s
 // (n tokens touch at most floor(n/P) + 2 pages), so the grid needs only the
 // packed total.  Memory-bound: every byte is moved once.
@@ -33,8 +36,9 @@ namespace sa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxCols = 256;   // D
-constexpr int kQTokens = 8;     // tokens per query CTA (one per warp)
+constexpr int kMaxD = 256;
+constexpr int kQTokens = 8;      // tokens per query CTA (one per warp)
+constexpr int kStage = 8192;     // 16-bit elements of keys staged at a time
 
 // Last b in [0, B) with key(b) <= x (key ascending, key(0) <= x); whole warp.
 template <typename F>
@@ -60,15 +64,17 @@ struct Pieces {   // one unit: 8 columns, or 8 + their 8 partners
   uint4 a, b;
 };
 
-// Rotate 8 pairs (a_k, b_k) of 16-bit pieces by c, s.
-SA_DEV void rotate_halves(Pieces& u, const float* __restrict__ cs, int r2, int k0) {
+// The cosines and sines of a unit's pairs: 8 of each (halves), or 4 (adjacent).
+struct Trig {
+  float4 c[2], s[2];
+};
+SA_DEV void rotate_halves(Pieces& u, const Trig& t) {
   uint32_t* pa = reinterpret_cast<uint32_t*>(&u.a);
   uint32_t* pb = reinterpret_cast<uint32_t*>(&u.b);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k0 + 4 * q));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + r2 + k0 + 4 * q));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    const float cc[4] = {t.c[q].x, t.c[q].y, t.c[q].z, t.c[q].w};
+    const float ss[4] = {t.s[q].x, t.s[q].y, t.s[q].z, t.s[q].w};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t wa = pa[2 * q + i], wb = pb[2 * q + i];
@@ -81,11 +87,9 @@ SA_DEV void rotate_halves(Pieces& u, const float* __restrict__ cs, int r2, int k
     }
   }
 }
-// Rotate the 4 adjacent pairs of one piece.
-SA_DEV void rotate_pairs(uint4& x, const float* __restrict__ cs, int r2, int k0) {
-  const float4 c = __ldg(reinterpret_cast<const float4*>(cs + k0));
-  const float4 s = __ldg(reinterpret_cast<const float4*>(cs + r2 + k0));
-  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+SA_DEV void rotate_pairs(uint4& x, const Trig& t) {
+  const float cc[4] = {t.c[0].x, t.c[0].y, t.c[0].z, t.c[0].w};
+  const float ss[4] = {t.s[0].x, t.s[0].y, t.s[0].z, t.s[0].w};
   uint32_t* p = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -112,11 +116,26 @@ SA_DEV void store_unit(uint16_t* row, int2 c, const Pieces& p) {
   *reinterpret_cast<uint4*>(row + c.x) = p.a;
   if (c.y >= 0) *reinterpret_cast<uint4*>(row + c.y) = p.b;
 }
-SA_DEV void rotate_unit(Pieces& p, int2 c, const float* cs, int r, bool inter) {
+// The trigonometry of the unit at columns c of a table row (none: unused).
+SA_DEV Trig load_trig(const float* __restrict__ cs, int2 c, int r, bool inter) {
+  Trig t = {};
+  if (c.y >= 0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      t.c[q] = __ldg(reinterpret_cast<const float4*>(cs + c.x + 4 * q));
+      t.s[q] = __ldg(reinterpret_cast<const float4*>(cs + r / 2 + c.x + 4 * q));
+    }
+  } else if (inter && c.x < r) {
+    t.c[0] = __ldg(reinterpret_cast<const float4*>(cs + c.x / 2));
+    t.s[0] = __ldg(reinterpret_cast<const float4*>(cs + r / 2 + c.x / 2));
+  }
+  return t;
+}
+SA_DEV void rotate_unit(Pieces& p, int2 c, const Trig& t, int r, bool inter) {
   if (c.y >= 0)
-    rotate_halves(p, cs, r / 2, c.x);
+    rotate_halves(p, t);
   else if (inter && c.x < r)
-    rotate_pairs(p.a, cs, r / 2, c.x / 2);
+    rotate_pairs(p.a, t);
 }
 
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendArgs a) {
@@ -138,19 +157,35 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
       if (lane == 0) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
       return;
     }
-    const float* cs = a.table + pos * r;
-    for (int x = lane; x < a.Hq * upr; x += 32) {
-      const int h = x / upr, u = x - h * upr;
-      const int2 c = unit_cols(u, r, inter);
-      Pieces p = load_unit(a.q + t * a.q0 + h * a.q1, c);
-      rotate_unit(p, c, cs, r, inter);
-      store_unit(a.q_out + ((int64_t)t * a.Hq + h) * D, c, p);
+    const int hpl = 32 / upr, u = lane % upr;   // heads per pass of the warp, this lane's unit
+    int h = lane / upr;
+    if (h >= hpl) return;
+    const int2 c = unit_cols(u, r, inter);
+    const Trig t_cs = load_trig(a.table + pos * r, c, r, inter);
+    const uint16_t* src = a.q + t * a.q0;
+    uint16_t* dst = a.q_out + (int64_t)t * a.Hq * D;
+    constexpr int kU = 4;   // heads in flight
+    for (; h + (kU - 1) * hpl < a.Hq; h += kU * hpl) {
+      Pieces p[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) p[k] = load_unit(src + (h + k * hpl) * a.q1, c);
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        rotate_unit(p[k], c, t_cs, r, inter);
+        store_unit(dst + (h + k * hpl) * D, c, p[k]);
+      }
+    }
+    for (; h < a.Hq; h += hpl) {
+      Pieces p = load_unit(src + h * a.q1, c);
+      rotate_unit(p, c, t_cs, r, inter);
+      store_unit(dst + h * D, c, p);
     }
     return;
   }
   // ================= one touched page of one kv head
-  __shared__ double sum_s[kThreads * 16];       // [row group][column]
-  __shared__ uint16_t exp_s[kThreads * 16];     // largest << 8 | smallest exponent field
+  __shared__ __align__(16) uint16_t key_s[kStage];   // a block of rows of keys
+  __shared__ double sum_s[kThreads];                 // [row group][column]
+  __shared__ uint16_t exp_s[kThreads];               // largest << 8 | smallest exponent field
   const int h = blockIdx.x % a.Hkv, s = blockIdx.x / a.Hkv;
   const int P = a.P;
   const int b = last_le(a.B, s, [&](int i) { return (int64_t)(a.cu[i] / P) + 2 * i; });
@@ -192,84 +227,82 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
     *reinterpret_cast<uint4*>(vpage + row * a.vs2 + c) =
         *reinterpret_cast<const uint4*>(a.v + (tok0 + row) * a.v0 + h * a.v1 + c);
   }
-  // ---- keys: rotated, stored and summed (old rows only summed)
-  const int groups = kThreads / upr;              // row groups; upr <= 32
+  // ---- keys, a block of rows at a time: the new ones rotated and stored, all of
+  // them staged; then one thread per column (and row group) sums
+  const int step = kThreads / upr;                 // rows per pass; upr <= 32
   const int g = tid / upr, u = tid - g * upr;
   const int2 c = unit_cols(u, r, inter);
-  const int ncol = c.y >= 0 ? 16 : 8;
-  double acc[16];
-  int emax[16], emin[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) acc[k] = 0.0, emax[k] = 0, emin[k] = 255;
-  if (g < groups) {
-    for (int row = a.sig ? g : n_old + g; row < nval; row += groups) {
-      Pieces x;
-      if (row < n_old) {
-        x = load_unit(kpage + row * a.ks2, c);
-      } else {
-        x = load_unit(a.k + (tok0 + row) * a.k0 + h * a.k1, c);
-        rotate_unit(x, c, a.table + (p0 + row) * r, r, inter);
-        store_unit(kpage + row * a.ks2, c, x);
-        if (a.k_out) store_unit(a.k_out + ((tok0 + row) * a.Hkv + h) * D, c, x);
-      }
-      if (a.sig) {
-        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t bits = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-          const int e = max(1, (int)((bits >> 7) & 0xffu));   // zeros: skipped below
-          if (bits & 0x7fffu) {
-            emax[k] = max(emax[k], e);
-            emin[k] = min(emin[k], e);
-          }
-          acc[k] += static_cast<double>(bf16_bits_to_float(bits));
+  const int block = kStage / D;                    // rows per block
+  const int groups = kThreads / D, d = tid % D, sg = tid / D;   // D <= 256
+  double sum = 0.0;
+  int emax = 0, emin = 255;
+  for (int r0 = a.sig ? 0 : n_old; r0 < nval; r0 += block) {
+    const int r1 = min(nval, r0 + block);
+    if (g < step) {
+      for (int row = r0 + g; row < r1; row += step) {
+        Pieces x;
+        if (row < n_old) {
+          x = load_unit(kpage + row * a.ks2, c);
+        } else {
+          x = load_unit(a.k + (tok0 + row) * a.k0 + h * a.k1, c);
+          rotate_unit(x, c, load_trig(a.table + (p0 + row) * r, c, r, inter), r, inter);
+          store_unit(kpage + row * a.ks2, c, x);
+          if (a.k_out) store_unit(a.k_out + ((tok0 + row) * a.Hkv + h) * D, c, x);
         }
+        if (a.sig) store_unit(key_s + (row - r0) * D, c, x);
       }
     }
+    if (!a.sig) continue;
+    __syncthreads();
+    if (sg < groups) {
+      for (int row = sg; row < r1 - r0; row += groups) {
+        const uint32_t bits = key_s[row * D + d];
+        if ((bits & 0x7fffu) == 0) continue;
+        const int e = max(1, (int)((bits >> 7) & 0xffu));
+        emax = max(emax, e);
+        emin = min(emin, e);
+        sum += static_cast<double>(bf16_bits_to_float(bits));
+      }
+    }
+    __syncthreads();
   }
   if (!a.sig) return;
-  if (g < groups) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (k >= ncol) continue;
-      const int d = k < 8 ? c.x + k : c.y + k - 8;
-      sum_s[g * D + d] = acc[k];
-      exp_s[g * D + d] = static_cast<uint16_t>(emax[k] << 8 | emin[k]);
-    }
+  if (sg < groups) {
+    sum_s[tid] = sum;
+    exp_s[tid] = static_cast<uint16_t>(emax << 8 | emin);
   }
   __syncthreads();
+  if (tid >= D) return;
   const int lg = 32 - __clz(nval);   // >= ceil(log2 nval) + 1
-  for (int d = tid; d < D; d += kThreads) {
-    double t = 0.0;
-    int hi = 0, lo = 255;
-    for (int q = 0; q < min(groups, nval); ++q) {
-      t += sum_s[q * D + d];
-      hi = max(hi, exp_s[q * D + d] >> 8);
-      lo = min(lo, exp_s[q * D + d] & 0xff);
-    }
-    // |x| < 2^(hi - 126) and a multiple of 2^(lo - 134): the float64 sum is
-    // exact in any order while that span and the carries fit 53 bits
-    if (hi > 0 && hi - lo + 8 + lg > 53) {
-      ExactAcc e;
-      e.clear();
-      for (int row = 0; row < nval; ++row) {   // this block's own stores: visible after the barrier
-        uint32_t m;
-        int ex;
-        bool neg;
-        bf16_fields(*(volatile uint16_t*)(kpage + row * a.ks2 + d), m, ex, neg);
-        e.add(m, ex, neg);
-      }
-      t = e.round_to_double();
-    }
-    a.sig[((int64_t)ph * a.Hkv + h) * D + d] = f64_to_bf16_rne(t / static_cast<double>(nval));
+  double t = 0.0;
+  int hi = 0, lo = 255;
+  for (int q = 0; q < groups; ++q) {
+    t += sum_s[q * D + tid];
+    hi = max(hi, exp_s[q * D + tid] >> 8);
+    lo = min(lo, exp_s[q * D + tid] & 0xff);
   }
+  // |x| < 2^(hi - 126) and a multiple of 2^(lo - 134): the float64 sum is exact in
+  // any order while that span and the carries fit 53 bits
+  if (hi > 0 && hi - lo + 8 + lg > 53) {
+    ExactAcc e;
+    e.clear();
+    for (int row = 0; row < nval; ++row) {   // this block's own stores: visible after the barriers
+      uint32_t m;
+      int ex;
+      bool neg;
+      bf16_fields(*(volatile uint16_t*)(kpage + row * a.ks2 + tid), m, ex, neg);
+      e.add(m, ex, neg);
+    }
+    t = e.round_to_double();
+  }
+  a.sig[((int64_t)ph * a.Hkv + h) * D + tid] = f64_to_bf16_rne(t / static_cast<double>(nval));
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
-  static_assert(kMaxCols / 8 <= 32, "a row's units fit one row group");
+  static_assert(kMaxD / 8 <= 32 && kMaxD <= kThreads, "a row's units fit a warp, its columns a CTA");
   // (page, kv head) CTAs first: their chains (search, table, page, sums) are the longest
   const int64_t pages = (int64_t)a.total / a.P + 2 * (int64_t)a.B;
   const int64_t page_ctas = pages * a.Hkv;
