@@ -847,73 +847,79 @@ def sa_append_kv_dir(k_new, v_new, n_new, k_cache, v_cache, page_dir, page_block
 # packed batches: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 of
 # [tokens, heads, D] tensors (cu [B + 1] int32 on the GPU)
 # ---------------------------------------------------------------------------
-# (these calls are short: what is checked per call is read once and cheaply)
+# These calls take microseconds on the GPU, so the host side is kept short: each
+# tensor's device, type and shape are looked at once.
 @functools.lru_cache(maxsize=1024)
 def _stride_array(strides) -> "ctypes.Array":
     return (ctypes.c_int64 * len(strides))(*strides)
 
 
-def _on_current(device: int):
-    """The calls launch on the current device's stream: tensors of another
-    device are refused rather than read from there."""
+def _ptrs(tensors, device: int):
+    """Data pointers (None for None); every tensor must be on `device`, the current
+    GPU: the calls launch there, and would read another device's memory from it."""
     if device < 0 or device != torch.cuda.current_device():
         raise ValueError("tensors must be on the current GPU")
+    keep = getattr(_REC, "keep", None)
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != device:
+            raise ValueError("tensors must be on the same GPU")
+        if keep is not None:
+            keep.append(t)
+        out.append(t.data_ptr())
+    return out
 
 
-def _same_gpu(t, device: int):
-    if t.get_device() != device:
-        raise ValueError("tensors must be on the same GPU")
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
 
 
-def _packed(t, heads, D, device, what):
+def _packed(t, heads, D, what):
     if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, D):
         raise TypeError(f"{what} must be a bfloat16 tensor [tokens, {heads}, {D}]")
-    _same_gpu(t, device)
 
 
-def _dense(t, dtype, shape, device, what):
+def _dense(t, dtype, shape, what):
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    _same_gpu(t, device)
 
 
-def _cache_pair(k_cache, v_cache, D, device):
+def _cache_pair(k_cache, v_cache, D):
     shape = k_cache.shape
     if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16
             or len(shape) != 4 or shape != v_cache.shape or shape[3] != D):
         raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    _same_gpu(k_cache, device), _same_gpu(v_cache, device)
     return shape
 
 
-def _error_word(dev_error, device):
-    if dev_error is not None and (dev_error.dtype is not torch.int32
-                                  or dev_error.get_device() != device):
-        raise TypeError("dev_error must be an int32 tensor on the same GPU")
-    return _ptr(dev_error)
-
-
-def _batch_of(cu, device, what):
+def _batch_of(cu, what):
     """B of the offsets cu [B + 1]"""
     if cu.dtype is not torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
         raise TypeError(f"{what} must be a contiguous int32 tensor [B + 1]")
-    _same_gpu(cu, device)
     return cu.shape[0] - 1
 
 
-def _flat_args(page_table, B, device):
+def _page_table(page_table, B):
     if page_table.dtype is not torch.int32 or page_table.dim() != 2 or \
             page_table.shape[0] != B or not page_table.is_contiguous():
         raise TypeError("page_table must be a contiguous int32 tensor [B, max_pages]")
-    _same_gpu(page_table, device)
-    return _ptr(page_table), page_table.shape[1]
+    return page_table.shape[1]
 
 
-def _dir_args_on(page_dir, page_blocks, block_shift, B, device):
-    _same_gpu(page_dir, device), _same_gpu(page_blocks, device)
+def _page_dir(page_dir, page_blocks, block_shift, B):
     if page_dir.dim() != 2 or page_dir.shape[0] != B:
         raise ValueError("page_dir must be [B, n_dir]")
-    return _dir_args(page_dir, page_blocks, block_shift)
+    _dir_args(page_dir, page_blocks, block_shift)
+
+
+def _error_word(dev_error):
+    if dev_error is not None and dev_error.dtype is not torch.int32:
+        raise TypeError("dev_error must be an int32 tensor")
 
 
 def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
@@ -923,45 +929,52 @@ def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
-def _dense_common(q, cu_q, Hkv, o_out, lse_out, workspace):
+def _dense_common(q, cu_q, Hkv, o_out, lse_out, workspace, dev_error):
     if q.dim() != 3 or q.dtype is not torch.bfloat16:
         raise TypeError("q must be a bfloat16 tensor [tokens, Hq, D]")
-    dev = q.get_device()
-    _on_current(dev)
     shape = q.shape
-    total, Hq, D = shape
-    B = _batch_of(cu_q, dev, "cu_q")
+    if not q.is_cuda:
+        raise ValueError("tensors must be on the current GPU")
     if o_out is None:
         o_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
-        _dense(o_out, torch.bfloat16, shape, dev, "o_out")
+        _dense(o_out, torch.bfloat16, shape, "o_out")
     if lse_out is None:
         lse_out = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
     else:
-        _dense(lse_out, torch.float32, shape[:2], dev, "lse_out")
+        _dense(lse_out, torch.float32, shape[:2], "lse_out")
     if workspace is None:
-        workspace = dense_attention_workspace(total, Hq, Hkv, D, q.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
-            workspace.get_device() != dev:
-        raise TypeError("workspace must be a contiguous uint8 tensor on the same GPU")
-    return dev, total, Hq, D, B, o_out, lse_out, workspace
+        workspace = dense_attention_workspace(shape[0], shape[1], Hkv, shape[2], q.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    _error_word(dev_error)
+    return shape, _batch_of(cu_q, "cu_q"), o_out, lse_out, workspace
 
 
-def _chunk(name, q, k_cache, v_cache, map_args, seq_lens, cu_q, scale, window, o_out, lse_out,
+def _chunk(q, k_cache, v_cache, page_map, seq_lens, cu_q, scale, window, o_out, lse_out,
            workspace, dev_error, stream):
     lib = load()
     if k_cache.dim() != 4:
         raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    dev, total, Hq, D, B, o_out, lse_out, workspace = _dense_common(
-        q, cu_q, k_cache.shape[1], o_out, lse_out, workspace)
-    P_pool, Hkv, P, _ = _cache_pair(k_cache, v_cache, D, dev)
-    _dense(seq_lens, torch.int32, (B,), dev, "seq_lens")
-    _call(getattr(lib, name),
-          (_ptr(q), _stride_array(q.stride()), _ptr(cu_q), total, _ptr(k_cache),
-           _stride_array(k_cache.stride()), _ptr(v_cache), _stride_array(v_cache.stride()),
-           *map_args(B, dev), _ptr(seq_lens), B, Hq, Hkv, D, P, P_pool, scale, window,
-           _ptr(o_out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
-           _error_word(dev_error, dev), _stream(stream)), name)
+    (total, Hq, D), B, o_out, lse_out, workspace = _dense_common(
+        q, cu_q, k_cache.shape[1], o_out, lse_out, workspace, dev_error)
+    P_pool, Hkv, P, _ = _cache_pair(k_cache, v_cache, D)
+    _dense(seq_lens, torch.int32, (B,), "seq_lens")
+    dev = q.get_device()
+    if len(page_map) == 1:
+        name, fn, blocks = "sa_chunk_attention", lib.sa_chunk_attention, None
+        n_map = _page_table(page_map[0], B)
+    else:
+        name, fn, blocks = "sa_chunk_attention_dir", lib.sa_chunk_attention_dir, page_map[1]
+        _page_dir(*page_map, B)
+    pq, pcu, pk, pv, pmap, pb, psl, po, pl, pw, pe = _ptrs(
+        (q, cu_q, k_cache, v_cache, page_map[0], blocks, seq_lens, o_out, lse_out, workspace,
+         dev_error), dev)
+    margs = (pmap, n_map) if blocks is None else (pmap, page_map[0].shape[1], pb,
+                                                  blocks.shape[0], page_map[2])
+    _call(fn, (pq, _stride_array(q.stride()), pcu, total, pk, _stride_array(k_cache.stride()), pv,
+               _stride_array(v_cache.stride()), *margs, psl, B, Hq, Hkv, D, P, P_pool, scale,
+               window, po, pl, pw, workspace.numel(), pe, _raw_stream(stream, dev)), name)
     return o_out, lse_out
 
 
@@ -973,18 +986,16 @@ def sa_chunk_attention(q, k_cache, v_cache, page_table, seq_lens, cu_q, scale: f
     cache [P_pool,Hkv,P,D]; window > 0 limits a token to its last `window` keys.  workspace:
     from dense_attention_workspace (a fresh one is made when omitted).  Returns (o
     [tokens,Hq,D] bf16, lse [tokens,Hq] f32); tokens behind cu_q[B] are left as they were."""
-    return _chunk("sa_chunk_attention", q, k_cache, v_cache,
-                  lambda B, dev: _flat_args(page_table, B, dev), seq_lens, cu_q, scale, window,
-                  o_out, lse_out, workspace, dev_error, stream)
+    return _chunk(q, k_cache, v_cache, (page_table,), seq_lens, cu_q, scale, window, o_out,
+                  lse_out, workspace, dev_error, stream)
 
 
 def sa_chunk_attention_dir(q, k_cache, v_cache, page_dir, page_blocks, block_shift: int, seq_lens,
                            cu_q, scale: float, window: int = 0, o_out=None, lse_out=None,
                            workspace=None, dev_error=None, stream=None):
     """sa_chunk_attention over a two-level page map."""
-    return _chunk("sa_chunk_attention_dir", q, k_cache, v_cache,
-                  lambda B, dev: _dir_args_on(page_dir, page_blocks, block_shift, B, dev),
-                  seq_lens, cu_q, scale, window, o_out, lse_out, workspace, dev_error, stream)
+    return _chunk(q, k_cache, v_cache, (page_dir, page_blocks, int(block_shift)), seq_lens, cu_q,
+                  scale, window, o_out, lse_out, workspace, dev_error, stream)
 
 
 def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_out=None,
@@ -996,36 +1007,35 @@ def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_ou
     if k.dim() != 3:
         raise TypeError("k must be a bfloat16 tensor [keys, Hkv, D]")
     Hkv = k.shape[1]
-    dev, total, Hq, D, B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
-                                                                    workspace)
-    _packed(k, Hkv, D, dev, "k"), _packed(v, Hkv, D, dev, "v")
+    (total, Hq, D), B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
+                                                                 workspace, dev_error)
+    _packed(k, Hkv, D, "k"), _packed(v, Hkv, D, "v")
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must hold the same tokens")
-    if _batch_of(cu_k, dev, "cu_k") != B:
+    if _batch_of(cu_k, "cu_k") != B:
         raise ValueError("cu_q and cu_k must hold the same sequences")
+    dev = q.get_device()
+    pq, pcu, pk, pv, pck, po, pl, pw, pe = _ptrs(
+        (q, cu_q, k, v, cu_k, o_out, lse_out, workspace, dev_error), dev)
     _call(lib.sa_prompt_attention,
-          (_ptr(q), _stride_array(q.stride()), _ptr(cu_q), total, _ptr(k),
-           _stride_array(k.stride()), _ptr(v), _stride_array(v.stride()), _ptr(cu_k), k.shape[0],
-           B, Hq, Hkv, D, scale, window, _ptr(o_out), _ptr(lse_out), _ptr(workspace),
-           workspace.numel(), _error_word(dev_error, dev), _stream(stream)),
-          "sa_prompt_attention")
+          (pq, _stride_array(q.stride()), pcu, total, pk, _stride_array(k.stride()), pv,
+           _stride_array(v.stride()), pck, k.shape[0], B, Hq, Hkv, D, scale, window, po, pl, pw,
+           workspace.numel(), pe, _raw_stream(stream, dev)), "sa_prompt_attention")
     return o_out, lse_out
 
 
-def _append_rope(name, q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, map_args,
-                 seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream):
+def _append_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page_map, seq_lens,
+                 summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream):
     lib = load()
     if k_new.dim() != 3 or k_new.dtype is not torch.bfloat16:
         raise TypeError("k_new must be a bfloat16 tensor [tokens, Hkv, D]")
-    dev = k_new.get_device()
-    _on_current(dev)
     total, Hkv, D = k_new.shape
-    _packed(v_new, Hkv, D, dev, "v_new")
+    _packed(v_new, Hkv, D, "v_new")
     if v_new.shape[0] != total:
         raise ValueError("k_new and v_new must hold the same tokens")
-    B = _batch_of(cu_new, dev, "cu_new")
-    _dense(seq_lens, torch.int32, (B,), dev, "seq_lens")
-    P_pool, heads, P, _ = _cache_pair(k_cache, v_cache, D, dev)
+    B = _batch_of(cu_new, "cu_new")
+    _dense(seq_lens, torch.int32, (B,), "seq_lens")
+    P_pool, heads, P, _ = _cache_pair(k_cache, v_cache, D)
     if heads != Hkv:
         raise ValueError("the caches must have k_new's heads")
     n_pos = rot = 0
@@ -1033,7 +1043,6 @@ def _append_rope(name, q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache
         if rope_table.dtype is not torch.float32 or rope_table.dim() != 2 or \
                 not rope_table.is_contiguous():
             raise TypeError("rope_table must be a contiguous float32 tensor [positions, rot_dim]")
-        _same_gpu(rope_table, dev)
         n_pos, rot = rope_table.shape
     Hq = 0
     qs = (0, 0, 1)
@@ -1041,27 +1050,38 @@ def _append_rope(name, q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache
         if q_new.dim() != 3 or q_new.shape[0] != total:
             raise ValueError("q_new must hold k_new's tokens")
         Hq = q_new.shape[1]
-        _packed(q_new, Hq, D, dev, "q_new")
+        _packed(q_new, Hq, D, "q_new")
         qs = q_new.stride()
         if q_out is None:
             q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q_new.device)
         else:
-            _dense(q_out, torch.bfloat16, (total, Hq, D), dev, "q_out")
+            _dense(q_out, torch.bfloat16, (total, Hq, D), "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q_new")
     if k_out is not None:
-        _dense(k_out, torch.bfloat16, (total, Hkv, D), dev, "k_out")
+        _dense(k_out, torch.bfloat16, (total, Hkv, D), "k_out")
     if summaries is not None:
-        _dense(summaries, torch.bfloat16, (P_pool, Hkv, D), dev, "summaries")
+        _dense(summaries, torch.bfloat16, (P_pool, Hkv, D), "summaries")
     if out_seq_lens is not None:
-        _dense(out_seq_lens, torch.int32, (B,), dev, "out_seq_lens")
-    _call(getattr(lib, name),
-          (_ptr(q_new), _stride_array(qs), _ptr(k_new), _stride_array(k_new.stride()),
-           _ptr(v_new), _stride_array(v_new.stride()), _ptr(cu_new), total, _ptr(rope_table),
-           n_pos, rot, 1 if interleaved else 0, _ptr(q_out), _ptr(k_out), _ptr(k_cache),
-           _stride_array(k_cache.stride()), _ptr(v_cache), _stride_array(v_cache.stride()),
-           *map_args(B, dev), _ptr(seq_lens), _ptr(out_seq_lens), B, Hq, Hkv, D, P, P_pool,
-           _ptr(summaries), _error_word(dev_error, dev), _stream(stream)), name)
+        _dense(out_seq_lens, torch.int32, (B,), "out_seq_lens")
+    _error_word(dev_error)
+    dev = k_new.get_device()
+    if len(page_map) == 1:
+        name, fn, blocks = "sa_append_kv_rope", lib.sa_append_kv_rope, None
+        n_map = _page_table(page_map[0], B)
+    else:
+        name, fn, blocks = "sa_append_kv_rope_dir", lib.sa_append_kv_rope_dir, page_map[1]
+        _page_dir(*page_map, B)
+    pq, pk, pv, pcu, pt, pqo, pko, pkc, pvc, pmap, pb, psl, pnl, psig, pe = _ptrs(
+        (q_new, k_new, v_new, cu_new, rope_table, q_out, k_out, k_cache, v_cache, page_map[0],
+         blocks, seq_lens, out_seq_lens, summaries, dev_error), dev)
+    margs = (pmap, n_map) if blocks is None else (pmap, page_map[0].shape[1], pb,
+                                                  blocks.shape[0], page_map[2])
+    _call(fn, (pq, _stride_array(qs), pk, _stride_array(k_new.stride()), pv,
+               _stride_array(v_new.stride()), pcu, total, pt, n_pos, rot, 1 if interleaved else 0,
+               pqo, pko, pkc, _stride_array(k_cache.stride()), pvc,
+               _stride_array(v_cache.stride()), *margs, psl, pnl, B, Hq, Hkv, D, P, P_pool, psig,
+               pe, _raw_stream(stream, dev)), name)
     return q_out, out_seq_lens
 
 
@@ -1074,9 +1094,9 @@ def sa_append_kv_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache,
     rewrite the touched pages' summaries (optional) in place.  q_new [tokens,Hq,D]
     (optional) is rotated into q_out, the rotated keys also go to k_out when given; both
     may be the inputs themselves.  Returns (q_out, out_seq_lens)."""
-    return _append_rope("sa_append_kv_rope", q_new, k_new, v_new, cu_new, rope_table, k_cache,
-                        v_cache, lambda B, dev: _flat_args(page_table, B, dev), seq_lens,
-                        summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream)
+    return _append_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, (page_table,),
+                        seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error,
+                        stream)
 
 
 def sa_append_kv_rope_dir(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page_dir,
@@ -1084,8 +1104,6 @@ def sa_append_kv_rope_dir(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_ca
                           interleaved: bool = False, q_out=None, k_out=None, out_seq_lens=None,
                           dev_error=None, stream=None):
     """sa_append_kv_rope over a two-level page map."""
-    return _append_rope("sa_append_kv_rope_dir", q_new, k_new, v_new, cu_new, rope_table, k_cache,
-                        v_cache,
-                        lambda B, dev: _dir_args_on(page_dir, page_blocks, block_shift, B, dev),
-                        seq_lens, summaries, interleaved, q_out, k_out, out_seq_lens, dev_error,
-                        stream)
+    return _append_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache,
+                        (page_dir, page_blocks, int(block_shift)), seq_lens, summaries,
+                        interleaved, q_out, k_out, out_seq_lens, dev_error, stream)

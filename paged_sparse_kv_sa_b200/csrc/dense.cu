@@ -54,7 +54,7 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;        // keys per tile
 constexpr int kM = 128;           // rows per tile
 constexpr int kMaxSegs = 32;      // segments planned at a time
-constexpr int kItemUnits = 1;     // an item's fixed cost, in tiles
+constexpr int kItemUnits = 2;     // an item's fixed cost, in tiles (8192-token prompt: 518, 490, 495 us for 1, 2, 3)
 constexpr int kMinUnits = 2;      // smallest share worth a CTA
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
@@ -507,30 +507,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           };
-          // 64 columns' loads in flight together: a tile's own, or (halves: each of
-          // the two threads of a row writes half of the columns) 32 of each tile's
+          // 32 columns at a time, in a loop that stays small (a whole row's worth of
+          // straight-line code ran into instruction fetches: 196 us for the packed
+          // prompts, 186 us so); halves: each of the two threads of a row writes half
+          const int c0 = halves ? w * (D / 64) : 0, c1 = halves ? c0 + D / 64 : D / 32;
 #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            float o[64];
-            float(&oa)[32] = *reinterpret_cast<float(*)[32]>(&o[0]);
-            float(&ob)[32] = *reinterpret_cast<float(*)[32]>(&o[32]);
-            const int ca = halves ? w * (D / 64) + c : 2 * c;
-            tc::ld32(o_col + ca * 32, oa);
-            tc::ld32(halves ? b_col + ca * 32 : o_col + ca * 32 + 32, ob);
+          for (int c = c0; c < c1; ++c) {
+            float o[32];
+            tc::ld32(o_col + c * 32, o);
             tc::wait_ld();
-            if (halves) {   // (an accumulator that was never written may hold anything)
+            // (an accumulator that was never written may hold anything)
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float x = use_a ? oa[k] * wa : 0.f;
-                oa[k] = empty ? 0.f : use_b ? fmaf(ob[k], wb, x) : x;
-              }
-              put(oa, ca);
-            } else {
+            for (int k = 0; k < 32; ++k) o[k] = empty || !use_a ? 0.f : o[k] * wa;
+            if (use_b) {
+              float ob[32];
+              tc::ld32(b_col + c * 32, ob);
+              tc::wait_ld();
 #pragma unroll
-              for (int k = 0; k < 64; ++k) o[k] = empty || !use_a ? 0.f : o[k] * wa;
-              put(oa, ca);
-              put(ob, ca + 1);
+              for (int k = 0; k < 32; ++k) o[k] = empty ? 0.f : fmaf(ob[k], wb, o[k]);
             }
+            put(o, c);
           }
           if (row_ok && !(halves && w)) {
             const float lse2 = empty ? -INFINITY : m_all + log2f(l_all);

@@ -311,7 +311,7 @@ struct RopeAppendArgs {
   int B, total, Hq, Hkv, D, P, P_pool;
   uint16_t* sig;           // [P_pool, Hkv, D] (optional)
   int32_t* err;
-  int page_ctas;           // set by the launcher
+  int page_ctas, page_heads;   // set by the launcher
 };
 cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream);
 

@@ -11,8 +11,9 @@
 // copied.  Every product and sum is one float32 rounding (no contraction), the
 // result one rounding to bf16: the stored bits are those of the plain formula.
 //
-// Two kinds of CTA share the launch.  A page CTA owns one (touched page, kv
-// head): it reads the page's old keys and rotates and writes the new ones in
+// Two kinds of CTA share the launch.  A page CTA owns some kv heads of a touched
+// page (as many as its stage holds when there are pages enough to fill the GPU,
+// so that their loads share one chain of look-ups; one otherwise): it reads the page's old keys and rotates and writes the new ones in
 // 16-byte pieces (both halves of a rotated pair in one thread), leaves them in
 // shared memory as well, and then sums each column in float64 from there (one
 // column per thread: few registers, so enough CTAs are resident to keep the
@@ -38,7 +39,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxD = 256;
 constexpr int kQTokens = 8;      // tokens per query CTA (one per warp)
-constexpr int kStage = 8192;     // 16-bit elements of keys staged at a time
+constexpr int kStage = 16384;    // 16-bit elements of keys staged at a time
 
 // Last b in [0, B) with key(b) <= x (key ascending, key(0) <= x); whole warp.
 template <typename F>
@@ -186,10 +187,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
   __shared__ __align__(16) uint16_t key_s[kStage];   // a block of rows of keys
   __shared__ double sum_s[kThreads];                 // [row group][column]
   __shared__ uint16_t exp_s[kThreads];               // largest << 8 | smallest exponent field
-  const int h = blockIdx.x % a.Hkv, s = blockIdx.x / a.Hkv;
+  const int hgroups = (a.Hkv + a.page_heads - 1) / a.page_heads;
+  const int h0 = (blockIdx.x % hgroups) * a.page_heads, s = blockIdx.x / hgroups;
+  const int hn = min(a.page_heads, a.Hkv - h0);
   const int P = a.P;
   const int b = last_le(a.B, s, [&](int i) { return (int64_t)(a.cu[i] / P) + 2 * i; });
-  const bool lead = tid == 0 && h == 0;
+  const bool lead = tid == 0 && h0 == 0;
   const int t0 = a.cu[b], t1 = a.cu[b + 1], L = a.seq_lens[b];
   const int j = s - (t0 / P + 2 * b);
   if (t0 < 0 || t1 < t0 || t1 > a.total) {
@@ -218,52 +221,111 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
   const int n_old = (int)(L > p0 ? L - p0 : 0);
   const int nval = (int)((end < p0 + P ? end : p0 + P) - p0);
   const int64_t tok0 = t0 + p0 - L;               // token of row 0 (rows >= n_old are new)
-  uint16_t* kpage = a.k_cache + ph * a.ks0 + h * a.ks1;
-  uint16_t* vpage = a.v_cache + ph * a.vs0 + h * a.vs1;
+  uint16_t* kpage = a.k_cache + ph * a.ks0 + h0 * a.ks1;
+  uint16_t* vpage = a.v_cache + ph * a.vs0 + h0 * a.vs1;
+  // A thread takes one piece of a row (x of `per`) for every ng-th head: threads
+  // that the pieces leave over take other heads.
+  auto spread = [&](int per, auto&& body) {
+    const int ng = per >= kThreads ? 1 : min(hn, kThreads / per);
+    const int xg = ng > 1 ? tid / per : 0;
+    if (xg >= ng) return;
+    for (int x = tid - xg * per; x < per; x += ng > 1 ? per : kThreads) body(x, xg, ng);
+  };
+  constexpr int kU = 4;   // heads in flight
   // ---- values: copied
   const int cpr = D / 8;
-  for (int x = tid; x < (nval - n_old) * cpr; x += kThreads) {
-    const int row = n_old + x / cpr, c = (x % cpr) * 8;
-    *reinterpret_cast<uint4*>(vpage + row * a.vs2 + c) =
-        *reinterpret_cast<const uint4*>(a.v + (tok0 + row) * a.v0 + h * a.v1 + c);
-  }
+  if (nval > n_old)
+    spread((nval - n_old) * cpr, [&](int x, int xg, int ng) {
+      const int row = n_old + x / cpr, c = (x % cpr) * 8;
+      const uint16_t* src = a.v + (tok0 + row) * a.v0 + h0 * a.v1 + c;
+      uint16_t* dst = vpage + row * a.vs2 + c;
+      for (int h = xg; h < hn; h += kU * ng) {
+        uint4 v[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+          if (h + k * ng < hn) v[k] = *reinterpret_cast<const uint4*>(src + (h + k * ng) * a.v1);
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+          if (h + k * ng < hn) *reinterpret_cast<uint4*>(dst + (h + k * ng) * a.vs1) = v[k];
+      }
+    });
   // ---- keys, a block of rows at a time: the new ones rotated and stored, all of
   // them staged; then one thread per column (and row group) sums
-  const int step = kThreads / upr;                 // rows per pass; upr <= 32
-  const int g = tid / upr, u = tid - g * upr;
-  const int2 c = unit_cols(u, r, inter);
-  const int block = kStage / D;                    // rows per block
-  const int groups = kThreads / D, d = tid % D, sg = tid / D;   // D <= 256
+  const int block = max(1, kStage / (hn * D));     // rows per block: the page's, when hn > 1
+  const int groups = max(1, kThreads / (hn * D));  // row groups
+  const int d = tid % D, sg = tid / D;             // D <= 256
   double sum = 0.0;
   int emax = 0, emin = 255;
-  for (int r0 = a.sig ? 0 : n_old; r0 < nval; r0 += block) {
-    const int r1 = min(nval, r0 + block);
-    if (g < step) {
-      for (int row = r0 + g; row < r1; row += step) {
-        Pieces x;
-        if (row < n_old) {
-          x = load_unit(kpage + row * a.ks2, c);
-        } else {
-          x = load_unit(a.k + (tok0 + row) * a.k0 + h * a.k1, c);
-          rotate_unit(x, c, load_trig(a.table + (p0 + row) * r, c, r, inter), r, inter);
-          store_unit(kpage + row * a.ks2, c, x);
-          if (a.k_out) store_unit(a.k_out + ((tok0 + row) * a.Hkv + h) * D, c, x);
-        }
-        if (a.sig) store_unit(key_s + (row - r0) * D, c, x);
+  auto add = [&](uint32_t bits) {
+    if ((bits & 0x7fffu) == 0) return;
+    const int e = max(1, (int)((bits >> 7) & 0xffu));
+    emax = max(emax, e);
+    emin = min(emin, e);
+    sum += static_cast<double>(bf16_bits_to_float(bits));
+  };
+  const int lg = 32 - __clz(nval);   // >= ceil(log2 nval) + 1
+  // the mean of column dd of head h0 + h from its float64 sum: |x| < 2^(hi - 126)
+  // and a multiple of 2^(lo - 134), so the sum is exact in any order while that
+  // span and the carries fit 53 bits
+  auto mean = [&](double t, int hi, int lo, int h, int dd) {
+    if (hi > 0 && hi - lo + 8 + lg > 53) {
+      ExactAcc e;
+      e.clear();
+      for (int row = 0; row < nval; ++row) {   // this CTA's own stores: visible after the barriers
+        uint32_t m;
+        int ex;
+        bool neg;
+        bf16_fields(*(volatile uint16_t*)(kpage + h * a.ks1 + row * a.ks2 + dd), m, ex, neg);
+        e.add(m, ex, neg);
       }
+      t = e.round_to_double();
     }
+    a.sig[((int64_t)ph * a.Hkv + h0 + h) * D + dd] =
+        f64_to_bf16_rne(t / static_cast<double>(nval));
+  };
+  for (int r0 = a.sig ? 0 : n_old; r0 < nval; r0 += block) {
+    const int nr = min(nval - r0, block);
+    spread(nr * upr, [&](int x, int xg, int ng) {
+      const int row = r0 + x / upr;
+      const int2 c = unit_cols(x % upr, r, inter);
+      uint16_t* cached = kpage + row * a.ks2;
+      if (row < n_old) {
+        for (int h = xg; h < hn; h += ng)
+          store_unit(key_s + (h * nr + row - r0) * D, c, load_unit(cached + h * a.ks1, c));
+        return;
+      }
+      const Trig t = load_trig(a.table + (p0 + row) * r, c, r, inter);
+      const uint16_t* src = a.k + (tok0 + row) * a.k0 + h0 * a.k1;
+      for (int h = xg; h < hn; h += kU * ng) {
+        Pieces y[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+          if (h + k * ng < hn) y[k] = load_unit(src + (h + k * ng) * a.k1, c);
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int hk = h + k * ng;
+          if (hk >= hn) continue;
+          rotate_unit(y[k], c, t, r, inter);
+          store_unit(cached + hk * a.ks1, c, y[k]);
+          if (a.k_out) store_unit(a.k_out + ((tok0 + row) * a.Hkv + h0 + hk) * D, c, y[k]);
+          if (a.sig) store_unit(key_s + (hk * nr + row - r0) * D, c, y[k]);
+        }
+      }
+    });
     if (!a.sig) continue;
     __syncthreads();
-    if (sg < groups) {
-      for (int row = sg; row < r1 - r0; row += groups) {
-        const uint32_t bits = key_s[row * D + d];
-        if ((bits & 0x7fffu) == 0) continue;
-        const int e = max(1, (int)((bits >> 7) & 0xffu));
-        emax = max(emax, e);
-        emin = min(emin, e);
-        sum += static_cast<double>(bf16_bits_to_float(bits));
+    if (hn > 1) {   // the whole page is staged
+      for (int x = tid; x < hn * D; x += kThreads) {
+        const int h = x / D, dd = x - h * D;
+        sum = 0.0;
+        emax = 0, emin = 255;
+        for (int row = 0; row < nval; ++row) add(key_s[(h * nval + row) * D + dd]);
+        mean(sum, emax, emin, h, dd);
       }
+      return;
     }
+    if (sg < groups)
+      for (int row = sg; row < nr; row += groups) add(key_s[row * D + d]);
     __syncthreads();
   }
   if (!a.sig) return;
@@ -273,7 +335,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
   }
   __syncthreads();
   if (tid >= D) return;
-  const int lg = 32 - __clz(nval);   // >= ceil(log2 nval) + 1
   double t = 0.0;
   int hi = 0, lo = 255;
   for (int q = 0; q < groups; ++q) {
@@ -281,21 +342,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
     hi = max(hi, exp_s[q * D + tid] >> 8);
     lo = min(lo, exp_s[q * D + tid] & 0xff);
   }
-  // |x| < 2^(hi - 126) and a multiple of 2^(lo - 134): the float64 sum is exact in
-  // any order while that span and the carries fit 53 bits
-  if (hi > 0 && hi - lo + 8 + lg > 53) {
-    ExactAcc e;
-    e.clear();
-    for (int row = 0; row < nval; ++row) {   // this block's own stores: visible after the barriers
-      uint32_t m;
-      int ex;
-      bool neg;
-      bf16_fields(*(volatile uint16_t*)(kpage + row * a.ks2 + tid), m, ex, neg);
-      e.add(m, ex, neg);
-    }
-    t = e.round_to_double();
-  }
-  a.sig[((int64_t)ph * a.Hkv + h) * D + tid] = f64_to_bf16_rne(t / static_cast<double>(nval));
+  mean(t, hi, lo, 0, tid);
 }
 
 }  // namespace
@@ -303,9 +350,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
 cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
   static_assert(kMaxD / 8 <= 32 && kMaxD <= kThreads, "a row's units fit a warp, its columns a CTA");
-  // (page, kv head) CTAs first: their chains (search, table, page, sums) are the longest
+  // page CTAs first: their chains (search, table, page, sums) are the longest
   const int64_t pages = (int64_t)a.total / a.P + 2 * (int64_t)a.B;
-  const int64_t page_ctas = pages * a.Hkv;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int stage_heads = kStage / (a.P * a.D) < 1 ? 1 : kStage / (a.P * a.D);
+  a.page_heads = pages * a.Hkv > 6 * sms ? (stage_heads < a.Hkv ? stage_heads : a.Hkv) : 1;
+  const int64_t page_ctas = pages * ((a.Hkv + a.page_heads - 1) / a.page_heads);
   const int64_t q_ctas = a.q ? (a.total + kQTokens - 1) / kQTokens : 0;
   if (page_ctas + q_ctas > 0x7fffffff) return cudaErrorInvalidValue;
   a.page_ctas = (int)page_ctas;
