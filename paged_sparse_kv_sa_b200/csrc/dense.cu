@@ -31,8 +31,8 @@
 //                 missing page loads zeros from an out-of-range coordinate);
 //   warp 10       the next item's queries by TMA as soon as their buffer frees (the
 //                 box is the group's heads of as many tokens as fit 128 rows);
-//                 it also zeroes the value rows past a sequence's end;
-//   warp 11       first plans the CTA's share.
+//   warp 11       first plans the CTA's share, and zeroes the value rows past a
+//                 sequence's end.
 // An item of at most 128 rows gives both tiles the same rows and every other
 // key tile each ("halves"); the two running softmaxes merge in the epilogue,
 // both accumulators being in the same TMEM lanes.
@@ -150,9 +150,9 @@ SA_DEV bool all_well(bool ok, volatile int* abort_flag) {
 // All threads of the CTA, from whichever role's code they are in.
 SA_DEV void cta_sync() { asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory"); }
 // Registers per thread after the roles part: the launch's 384 x 168 divided as
-// 256 x 200 for the softmax warps (a row of scores is 128 registers) + 128 x 104.
-SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
-SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
+// 256 x 192 for the softmax warps (a row of scores is 128 registers) + 128 x 120.
+SA_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
+SA_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 120;"); }
 // A value every lane holds alike, as the compiler can see.
 template <typename T>
 SA_DEV T uni(T x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -243,9 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_s = smem + 2 * C::kQBytes;
   uint8_t* v_s = k_s + C::kStages * C::kTileBytes;
   __shared__ uint64_t k_full[C::kStages], k_empty[C::kStages];
-  __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages];
+  __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages], v_tail[C::kStages];
   __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty;
-  __shared__ uint64_t v_tail, v_tail_seen;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, n_segs_s, last_s;
   __shared__ Seg seg_s[kMaxSegs];
@@ -265,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
+      mbar_init(&v_tail[s], 32);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
@@ -274,8 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
-    mbar_init(&v_tail, 32);
-    mbar_init(&v_tail_seen, 1);
     abort_s = 0;
     fence_mbar_init();
     a.part_head[cta * 8] = 0;   // no part of this CTA starts an item, so far
@@ -565,16 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         cta_sync();
       }
     } else if (warp == kQWarp) {
-      // ================= queries; value rows past a sequence's end
-      uint32_t tails = 0;
+      // ================= queries
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
         last = last_s;
         for (int i = 0; i < n_segs && ok; ++i) {
           const Seg& s = seg_s[i];
-          const int nt = s.j1 - s.j0, j = s.j1 - 1;
-          if (nt == 0) continue;
+          if (s.j0 == s.j1) continue;
           ok = all_well((qc == 0 || wait(&q_empty, (qc - 1) & 1)) && !*abort_flag, abort_flag);
           if (!ok) break;
           // one box per tile and 64-column chunk; rows of other sequences' tokens
@@ -588,28 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s.kvh * G, s.q0 + s.r0 / G + w * a.tile_toks, 0);
           }
           ++qc;
-          // the rows may hold anything (0 * NaN): zeroed in the tile, up to the
-          // 16-key step that is multiplied
-          const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
-          const int rows = 16 * min(8, (hi - j * kKeys + 15) / 16), z0 = s.L - j * kKeys;
-          if (z0 < rows) {
-            const uint32_t c = kc + nt - 1;
-            const int st = c % C::kStages;
-            ok = wait(&v_full[st], (c / C::kStages) & 1);
-            uint8_t* vt = v_s + st * C::kTileBytes;
-            for (int x = lane; x < (rows - z0) * C::kChunks * 8; x += 32) {
-              const int row = z0 + x / (C::kChunks * 8), p = x % (C::kChunks * 8);
-              *reinterpret_cast<uint4*>(vt + (p >> 3) * (kKeys * 128) + row * 128 + (p & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_proxy_async();
-            // one tail at a time: v_tail has a single phase to wait for
-            if (tails > 0) ok = wait(&v_tail_seen, (tails - 1) & 1) && ok;
-            ok = all_well(ok, abort_flag);
-            mbar_arrive(&v_tail);
-            ++tails;
-          }
-          kc += nt;
         }
         cta_sync();
       }
@@ -621,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_desc = uni(tc::desc_lo(smem_u32(k_s), 16));
       const uint32_t v_desc = uni(tc::desc_lo(smem_u32(v_s), kKeys * 128));
       const uint32_t tmem_u = uni(tmem);
-      uint32_t tails = 0;
+      uint32_t tails = 0;   // bit st: phase of v_tail[st]
       // One run of an item's tiles.  halves: each row tile has every other key tile.
       auto run = [&](int j0, int nt, int L, int hi, auto hv) {
         constexpr bool halves = decltype(hv)::value != 0;
@@ -666,9 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h == 0 && (halves || w == 0)) {
               ok = wait(&v_full[st], (c / C::kStages) & 1) && ok;
               if (L - j * kKeys < 16 * steps) {   // rows past the end: zeroed first
-                ok = wait(&v_tail, tails & 1) && ok;
-                if (lane == 0) mbar_arrive(&v_tail_seen);
-                ++tails;
+                ok = wait(&v_tail[st], (tails >> st) & 1) && ok;
+                tails ^= 1u << st;
               }
             }
             tc::fence_after_sync();
@@ -821,9 +794,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_segs = n_segs_s;
         for (int i = 0; i < n_segs && ok; ++i) {   // V tiles
           const Seg s = seg_s[i];
-          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc)
+          const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
+          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc) {
             ok = load_tile<D>(box_of(a, s, j, lane), s.kvh, kc, v_s, &vmap, v_full, v_empty, a.box,
                               abort_flag);
+            // Value rows past the sequence's end may hold anything (0 * NaN): zeroed,
+            // up to the 16-key step that is multiplied (only in an item's last tile).
+            const int z0 = s.L - j * kKeys, nz = 16 * min(8, (hi - j * kKeys + 15) / 16) - z0;
+            if (nz > 0 && ok) {
+              const int st = kc % C::kStages;
+              ok = all_well(wait(&v_full[st], (kc / C::kStages) & 1), abort_flag);
+              uint8_t* vt = v_s + st * C::kTileBytes + z0 * 128;
+              for (int x = lane; x < nz * 8; x += 32)
+#pragma unroll
+                for (int ch = 0; ch < C::kChunks; ++ch)
+                  *reinterpret_cast<uint4*>(vt + ch * (kKeys * 128) + x * 16) =
+                      make_uint4(0, 0, 0, 0);
+              tc::fence_proxy_async();
+              mbar_arrive(&v_tail[st]);
+            }
+          }
         }
         cta_sync();
       } while (!last);

@@ -139,7 +139,7 @@ SA_DEV void rotate_unit(Pieces& p, int2 c, const Trig& t, int r, bool inter) {
     rotate_pairs(p.a, t);
 }
 
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppendArgs a) {
   pdl_wait_and_release();
   const int tid = threadIdx.x, lane = tid & 31;
   const int D = a.D, r = a.rot;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
     const Trig t_cs = load_trig(a.table + pos * r, c, r, inter);
     const uint16_t* src = a.q + t * a.q0;
     uint16_t* dst = a.q_out + (int64_t)t * a.Hq * D;
-    constexpr int kU = 4;   // heads in flight
+    constexpr int kU = 2;   // heads in flight
     for (; h + (kU - 1) * hpl < a.Hq; h += kU * hpl) {
       Pieces p[kU];
 #pragma unroll
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
     if (xg >= ng) return;
     for (int x = tid - xg * per; x < per; x += ng > 1 ? per : kThreads) body(x, xg, ng);
   };
-  constexpr int kU = 4;   // heads in flight
+  constexpr int kU = 2;   // heads in flight
   // ---- values: copied
   const int cpr = D / 8;
   if (nval > n_old)

@@ -330,3 +330,79 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for (o, lse), (wo, wl, _) in zip(outs, want):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+# ------------------------------------------------------------------ loads that fill the GPU
+def dense64(q, k, v, scale, window):
+    """O.dense_attention for one sequence, in float64 torch operations on the GPU."""
+    (n, Hq, D), (L, Hkv, _) = q.shape, k.shape
+    if L == 0:
+        z = torch.zeros((n, Hq, D), dtype=torch.float64, device=q.device)
+        return z, torch.full((n, Hq), -math.inf, dtype=torch.float64, device=q.device), z, z[..., 0]
+    qd = q.double().view(n, Hkv, Hq // Hkv, D)
+    kd, vd = k.double(), v.double()
+    s = scale * torch.einsum("nhgd,lhd->nhgl", qd, kd)
+    p, j = L - n + torch.arange(n, device=q.device)[:, None], torch.arange(L, device=q.device)[None, :]
+    seen = (j <= p) & (j > p - (window or L + n + 1))
+    s = s.masked_fill(~seen[:, None, None], -math.inf)
+    lse = torch.logsumexp(s, -1)
+    w = torch.where(lse[..., None] > -math.inf, torch.exp(s - lse[..., None]), torch.zeros_like(s))
+    reach = scale * torch.einsum("nhgd,lhd->nhgl", qd.abs(), kd.abs()).masked_fill(~seen[:, None, None], 0.0).amax(-1)
+    return (torch.einsum("nhgl,lhd->nhgd", w, vd).reshape(n, Hq, D), lse.view(n, Hq),
+            torch.einsum("nhgl,lhd->nhgd", w, vd.abs()).reshape(n, Hq, D), reach.view(n, Hq))
+
+
+def check64(o, lse, q, ks, vs, ns, scale, window):
+    """check() on the GPU: the same tolerances."""
+    at = 0
+    for n, k, v in zip(ns, ks, vs):
+        if n == 0:
+            continue
+        D = q.shape[2]
+        ro, rl, A, reach = dense64(q[at:at + n], k, v, scale, window)
+        eta = (D + 4) * 2.0 ** -23 * reach + 2.0 ** -21
+        tol = U * (A + ro.abs()) * (1 + U) + 4 * eta[..., None] * A
+        off = (o[at:at + n].double() - ro).abs() - tol
+        assert bool((off <= 0).all()), (float(off.max()), n, k.shape)
+        seen = rl > -math.inf
+        assert bool((lse[at:at + n][~seen] == -math.inf).all())
+        tl = eta + (20 + k.shape[0] / 128) * 2.0 ** -24 + 2.0 ** -22 * torch.where(seen, rl, torch.zeros_like(rl)).abs()
+        assert bool(((lse[at:at + n].double() - rl).abs()[seen] <= tl[seen]).all())
+        at += n
+
+
+LOADS = [
+    # B, n_lo, n_hi, L_lo, L_hi, G, Hkv, D, P, window: many ragged tiles in every CTA's share
+    (64, 1, 1, 500, 3000, 2, 8, 128, 16, 0),          # single tokens
+    (24, 2, 8, 900, 6000, 8, 8, 128, 64, 0),          # drafts
+    (16, 1, 400, 1000, 4000, 4, 8, 128, 16, 0),       # chunks between single tokens
+    (64, 1, 1, 500, 3000, 4, 8, 64, 48, 0),
+    (20, 1, 300, 300, 2500, 3, 8, 64, 128, 700),
+]
+
+
+@pytest.mark.parametrize("B,n_lo,n_hi,L_lo,L_hi,G,Hkv,D,P,window", LOADS)
+def test_chunk_under_load(B, n_lo, n_hi, L_lo, L_hi, G, Hkv, D, P, window):
+    rng = np.random.default_rng(B * D + n_hi)
+    ns = [int(x) for x in rng.integers(n_lo, n_hi + 1, B)]
+    Ls = [int(x) for x in rng.integers(L_lo, L_hi + 1, B)]
+    Ls = [max(n, L) for n, L in zip(ns, Ls)]
+    c = chunk_case(50 + B + D, ns, Ls, G, Hkv, D, P)
+    for _ in range(3):
+        o, lse, err = run_chunk(c, window)
+        assert err == 0
+        check64(o, lse, c["q"], c["ks"], c["vs"], ns, c["scale"], window)
+
+
+@pytest.mark.parametrize("B,lo,hi,G,Hkv,D,window", [(12, 150, 2048, 4, 8, 128, 0), (30, 1, 700, 4, 8, 64, 0),
+                                                  (3, 2000, 3001, 4, 8, 64, 1024), (9, 100, 900, 5, 6, 128, 333)])
+def test_prompt_under_load(B, lo, hi, G, Hkv, D, window):
+    rng = np.random.default_rng(B * D + hi)
+    ns = [int(x) for x in rng.integers(lo, hi + 1, B)]
+    g = torch.Generator().manual_seed(B)
+    q, k, v = (_randn(g, sum(ns), h, D) for h in (G * Hkv, Hkv, Hkv))
+    cu = _cu(ns)
+    ks, vs = torch.split(k, ns), torch.split(v, ns)
+    for _ in range(3):
+        o, lse = sa.sa_prompt_attention(q, k, v, cu, cu, 1.0 / math.sqrt(D), window=window)
+        check64(o, lse, q, ks, vs, ns, 1.0 / math.sqrt(D), window)

@@ -83,6 +83,9 @@ CASES = [
     ([50], [20], 4, 2, 72, 16, 16, False),            # most of the head unrotated, an odd width
     ([1] * 70, list(range(70)), 2, 1, 64, 16, 64, False),
     ([600], [13], 1, 1, 128, 512, 128, False),        # a page of many rows
+    ([900, 3, 700, 0, 650], [5, 60, 0, 9, 31], 8, 8, 128, 16, 128, False),   # pages enough for several heads a CTA
+    ([700, 1200], [3, 40], 5, 5, 64, 16, 32, True),
+    ([900, 2000], [70, 1], 2, 16, 128, 64, 64, False),
 ]
 
 
