@@ -58,6 +58,7 @@ constexpr int kItemUnits = 2;     // an item's fixed cost, in tiles (8192-token 
 constexpr int kMinUnits = 2;      // smallest share worth a CTA
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
+constexpr int kFewRows = 16;      // items of so few query rows have them copied by a warp
 constexpr int kStageRow = 80;     // bytes: 64 + 16 against bank conflicts
 static_assert(kDenseMaxBatch * 4 <= kSoftWarps * 32 * kStageRow, "the units fit the stage");
 
@@ -306,6 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftWarps) {
     // ================= softmax and epilogue
     regs_up();
+    for (int x = tid; x < C::kQBytes / 16; x += kSoftWarps * 32)   // tile A's queries: zero
+      reinterpret_cast<uint4*>(q_s)[x] = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async();
     for (bool last = false; !last;) {
       cta_sync();
       const int n_segs = n_segs_s;
@@ -564,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kQWarp) {
       // ================= queries
+      int q_rows = 0;   // rows of tile A's queries that may not be zero
       for (bool last = false; !last;) {
         cta_sync();
         const int n_segs = n_segs_s;
@@ -573,6 +578,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s.j0 == s.j1) continue;
           ok = all_well((qc == 0 || wait(&q_empty, (qc - 1) & 1)) && !*abort_flag, abort_flag);
           if (!ok) break;
+          if (s.nr <= kFewRows) {
+            // Few rows: copied by the warp, the tile's other rows zero.  (Boxes would
+            // bring other tokens' rows along: products nobody needs, at a power that
+            // lowers the clock -- 16 x 32K-key decode under load 424 us with, 410 us
+            // without them.)
+            constexpr int kPieces = D / 8;
+            auto at = [&](int row, int pc) {
+              return q_s + (pc >> 3) * (kM * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
+            };
+            const uint16_t* src = a.q + (s.q0 + s.r0 / G) * a.q0 + (int64_t)s.kvh * G * a.q1;
+            for (int x0 = lane; x0 < s.nr * kPieces; x0 += 32 * 4) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int row = (x0 + 32 * k) / kPieces, pc = (x0 + 32 * k) % kPieces, t = row / G;
+                if (row < s.nr)
+                  v[k] = *reinterpret_cast<const uint4*>(src + t * a.q0 + (row - t * G) * a.q1 +
+                                                         pc * 8);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int row = (x0 + 32 * k) / kPieces, pc = (x0 + 32 * k) % kPieces;
+                if (row < s.nr) *reinterpret_cast<uint4*>(at(row, pc)) = v[k];
+              }
+            }
+            for (int x = s.nr * kPieces + lane; x < q_rows * kPieces; x += 32)
+              *reinterpret_cast<uint4*>(at(x / kPieces, x % kPieces)) = make_uint4(0, 0, 0, 0);
+            q_rows = s.nr;
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+            ++qc;
+            continue;
+          }
+          q_rows = kM;
           // one box per tile and 64-column chunk; rows of other sequences' tokens
           // that a box holds are never kept, tokens past the tensor load as zeros
           const int tiles = s.nr > tile_rows ? 2 : 1;
