@@ -10,7 +10,6 @@ missing; calls raise instead.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -847,30 +846,35 @@ def sa_append_kv_dir(k_new, v_new, n_new, k_cache, v_cache, page_dir, page_block
 # packed batches: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 of
 # [tokens, heads, D] tensors (cu [B + 1] int32 on the GPU)
 # ---------------------------------------------------------------------------
-# These calls take microseconds on the GPU, so the host side is kept short: each
-# tensor's device, type and shape are looked at once.
-@functools.lru_cache(maxsize=1024)
-def _stride_array(strides) -> "ctypes.Array":
-    return (ctypes.c_int64 * len(strides))(*strides)
+# These calls take microseconds on the GPU, so the host side is kept short: one
+# condition over all tensors that are as they should be, and the words for what is
+# not only once it fails.
+_STRIDES = {}
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _ptrs(tensors, device: int):
+def _stride_array(t) -> "ctypes.Array":
+    s = t.stride()
+    a = _STRIDES.get(s)
+    if a is None:
+        if len(_STRIDES) > 4096:
+            _STRIDES.clear()
+        a = _STRIDES[s] = (ctypes.c_int64 * len(s))(*s)
+    return a
+
+
+def _ptrs(device: int, *tensors):
     """Data pointers (None for None); every tensor must be on `device`, the current
     GPU: the calls launch there, and would read another device's memory from it."""
     if device < 0 or device != torch.cuda.current_device():
         raise ValueError("tensors must be on the current GPU")
-    keep = getattr(_REC, "keep", None)
-    out = []
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != device:
+        if t is not None and t.get_device() != device:
             raise ValueError("tensors must be on the same GPU")
-        if keep is not None:
-            keep.append(t)
-        out.append(t.data_ptr())
-    return out
+    keep = getattr(_REC, "keep", None)
+    if keep is not None:
+        keep.extend(t for t in tensors if t is not None)
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -879,47 +883,38 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream
 
 
-def _packed(t, heads, D, what):
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise TypeError(f"{what} must be a bfloat16 tensor [tokens, {heads}, {D}]")
+def _like(t, dtype, shape, what, contiguous=True):
+    """Raise unless t (None: passes) has this type and shape, and is contiguous."""
+    if t is None:
+        return
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise TypeError(f"{what} must be contiguous")
 
 
-def _dense(t, dtype, shape, what):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise TypeError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-
-
-def _cache_pair(k_cache, v_cache, D):
-    shape = k_cache.shape
-    if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16
-            or len(shape) != 4 or shape != v_cache.shape or shape[3] != D):
-        raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    return shape
-
-
-def _batch_of(cu, what):
+def _offsets(cu, what):
     """B of the offsets cu [B + 1]"""
-    if cu.dtype is not torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+    if cu.dtype is not _I32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
         raise TypeError(f"{what} must be a contiguous int32 tensor [B + 1]")
     return cu.shape[0] - 1
 
 
-def _page_table(page_table, B):
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or \
-            page_table.shape[0] != B or not page_table.is_contiguous():
-        raise TypeError("page_table must be a contiguous int32 tensor [B, max_pages]")
-    return page_table.shape[1]
+def _rank(t, n, what):
+    if t.dim() != n or t.dtype is not _BF16:
+        raise TypeError(f"{what} must be a bfloat16 tensor of {n} dimensions")
+    return t.shape
 
 
-def _page_dir(page_dir, page_blocks, block_shift, B):
-    if page_dir.dim() != 2 or page_dir.shape[0] != B:
-        raise ValueError("page_dir must be [B, n_dir]")
-    _dir_args(page_dir, page_blocks, block_shift)
-
-
-def _error_word(dev_error):
-    if dev_error is not None and dev_error.dtype is not torch.int32:
-        raise TypeError("dev_error must be an int32 tensor")
+def _map_of(page_map, B):
+    """(device tensor, blocks or None, the C call's sizes) of a flat or two-level map"""
+    table = page_map[0]
+    if table.dtype is not _I32 or table.dim() != 2 or table.shape[0] != B or \
+            not table.is_contiguous():
+        raise TypeError("the page table or directory must be a contiguous int32 tensor [B, n]")
+    if len(page_map) > 1:
+        _dir_args(*page_map)
+    return table.shape[1]
 
 
 def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
@@ -929,52 +924,62 @@ def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
-def _dense_common(q, cu_q, Hkv, o_out, lse_out, workspace, dev_error):
-    if q.dim() != 3 or q.dtype is not torch.bfloat16:
-        raise TypeError("q must be a bfloat16 tensor [tokens, Hq, D]")
-    shape = q.shape
+def _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace, dev_error):
+    """The outputs and workspace of a dense call, made where they are not given."""
     if not q.is_cuda:
         raise ValueError("tensors must be on the current GPU")
     if o_out is None:
-        o_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _dense(o_out, torch.bfloat16, shape, "o_out")
+        o_out = torch.empty(shape, dtype=_BF16, device=q.device)
     if lse_out is None:
-        lse_out = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-    else:
-        _dense(lse_out, torch.float32, shape[:2], "lse_out")
+        lse_out = torch.empty(shape[:2], dtype=_F32, device=q.device)
     if workspace is None:
         workspace = dense_attention_workspace(shape[0], shape[1], Hkv, shape[2], q.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 tensor")
-    _error_word(dev_error)
-    return shape, _batch_of(cu_q, "cu_q"), o_out, lse_out, workspace
+    _like(o_out, _BF16, shape, "o_out")
+    _like(lse_out, _F32, shape[:2], "lse_out")
+    _like(workspace, torch.uint8, workspace.shape, "workspace")
+    if dev_error is not None and dev_error.dtype is not _I32:
+        raise TypeError("dev_error must be an int32 tensor")
+    return o_out, lse_out, workspace
+
+
+def _dense_fine(shape, o_out, lse_out, workspace, dev_error):
+    return (o_out is not None and lse_out is not None and workspace is not None
+            and o_out.dtype is _BF16 and lse_out.dtype is _F32
+            and workspace.dtype is torch.uint8 and o_out.shape == shape
+            and lse_out.shape == shape[:2] and o_out.is_contiguous()
+            and lse_out.is_contiguous() and workspace.is_contiguous()
+            and (dev_error is None or dev_error.dtype is _I32))
 
 
 def _chunk(q, k_cache, v_cache, page_map, seq_lens, cu_q, scale, window, o_out, lse_out,
            workspace, dev_error, stream):
-    lib = load()
-    if k_cache.dim() != 4:
-        raise TypeError("k_cache and v_cache must be bfloat16 tensors [P_pool, Hkv, P, D]")
-    (total, Hq, D), B, o_out, lse_out, workspace = _dense_common(
-        q, cu_q, k_cache.shape[1], o_out, lse_out, workspace, dev_error)
-    P_pool, Hkv, P, _ = _cache_pair(k_cache, v_cache, D)
-    _dense(seq_lens, torch.int32, (B,), "seq_lens")
+    lib = _lib or load()
+    shape = total, Hq, D = _rank(q, 3, "q")
+    P_pool, Hkv, P, _ = kshape = _rank(k_cache, 4, "k_cache")
+    B = _offsets(cu_q, "cu_q")
+    n_map = _map_of(page_map, B)
+    if not (v_cache.dtype is _BF16 and kshape == v_cache.shape and kshape[3] == D
+            and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()):
+        _like(v_cache, _BF16, (*kshape[:3], D), "v_cache", contiguous=False)
+        _like(k_cache, _BF16, v_cache.shape, "k_cache", contiguous=False)
+        _like(seq_lens, _I32, (B,), "seq_lens")
+    if not _dense_fine(shape, o_out, lse_out, workspace, dev_error):
+        o_out, lse_out, workspace = _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace,
+                                                   dev_error)
     dev = q.get_device()
-    if len(page_map) == 1:
-        name, fn, blocks = "sa_chunk_attention", lib.sa_chunk_attention, None
-        n_map = _page_table(page_map[0], B)
+    flat = len(page_map) == 1
+    pq, pcu, pk, pv, pm, pb, psl, po, pl, pw, pe = _ptrs(
+        dev, q, cu_q, k_cache, v_cache, page_map[0], None if flat else page_map[1], seq_lens,
+        o_out, lse_out, workspace, dev_error)
+    rest = (psl, B, Hq, Hkv, D, P, P_pool, scale, window, po, pl, pw, workspace.numel(), pe,
+            _raw_stream(stream, dev))
+    head = (pq, _stride_array(q), pcu, total, pk, _stride_array(k_cache), pv,
+            _stride_array(v_cache), pm, n_map)
+    if flat:
+        _call(lib.sa_chunk_attention, head + rest, "sa_chunk_attention")
     else:
-        name, fn, blocks = "sa_chunk_attention_dir", lib.sa_chunk_attention_dir, page_map[1]
-        _page_dir(*page_map, B)
-    pq, pcu, pk, pv, pmap, pb, psl, po, pl, pw, pe = _ptrs(
-        (q, cu_q, k_cache, v_cache, page_map[0], blocks, seq_lens, o_out, lse_out, workspace,
-         dev_error), dev)
-    margs = (pmap, n_map) if blocks is None else (pmap, page_map[0].shape[1], pb,
-                                                  blocks.shape[0], page_map[2])
-    _call(fn, (pq, _stride_array(q.stride()), pcu, total, pk, _stride_array(k_cache.stride()), pv,
-               _stride_array(v_cache.stride()), *margs, psl, B, Hq, Hkv, D, P, P_pool, scale,
-               window, po, pl, pw, workspace.numel(), pe, _raw_stream(stream, dev)), name)
+        _call(lib.sa_chunk_attention_dir, head + (pb, page_map[1].shape[0], page_map[2]) + rest,
+              "sa_chunk_attention_dir")
     return o_out, lse_out
 
 
@@ -1003,85 +1008,87 @@ def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_ou
     """Exact causal attention over whole packed prompts: q [tokens,Hq,D], k and v
     [keys,Hkv,D], sequence b at cu_q[b] .. and cu_k[b] .. (normally the same tensor), its
     queries the last of its key positions.  Returns (o [tokens,Hq,D] bf16, lse)."""
-    lib = load()
-    if k.dim() != 3:
-        raise TypeError("k must be a bfloat16 tensor [keys, Hkv, D]")
-    Hkv = k.shape[1]
-    (total, Hq, D), B, o_out, lse_out, workspace = _dense_common(q, cu_q, Hkv, o_out, lse_out,
-                                                                 workspace, dev_error)
-    _packed(k, Hkv, D, "k"), _packed(v, Hkv, D, "v")
-    if k.shape[0] != v.shape[0]:
-        raise ValueError("k and v must hold the same tokens")
-    if _batch_of(cu_k, "cu_k") != B:
-        raise ValueError("cu_q and cu_k must hold the same sequences")
+    lib = _lib or load()
+    shape = total, Hq, D = _rank(q, 3, "q")
+    total_k, Hkv, _ = kshape = _rank(k, 3, "k")
+    B = _offsets(cu_q, "cu_q")
+    if not (v.dtype is _BF16 and v.shape == kshape and kshape[2] == D
+            and cu_k.dtype is _I32 and cu_k.shape == (B + 1,) and cu_k.is_contiguous()):
+        _like(k, _BF16, (total_k, Hkv, D), "k", contiguous=False)
+        _like(v, _BF16, kshape, "v", contiguous=False)
+        _like(cu_k, _I32, (B + 1,), "cu_k")
+    if not _dense_fine(shape, o_out, lse_out, workspace, dev_error):
+        o_out, lse_out, workspace = _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace,
+                                                   dev_error)
     dev = q.get_device()
-    pq, pcu, pk, pv, pck, po, pl, pw, pe = _ptrs(
-        (q, cu_q, k, v, cu_k, o_out, lse_out, workspace, dev_error), dev)
+    pq, pcu, pk, pv, pck, po, pl, pw, pe = _ptrs(dev, q, cu_q, k, v, cu_k, o_out, lse_out,
+                                                 workspace, dev_error)
     _call(lib.sa_prompt_attention,
-          (pq, _stride_array(q.stride()), pcu, total, pk, _stride_array(k.stride()), pv,
-           _stride_array(v.stride()), pck, k.shape[0], B, Hq, Hkv, D, scale, window, po, pl, pw,
-           workspace.numel(), pe, _raw_stream(stream, dev)), "sa_prompt_attention")
+          (pq, _stride_array(q), pcu, total, pk, _stride_array(k), pv, _stride_array(v), pck,
+           total_k, B, Hq, Hkv, D, scale, window, po, pl, pw, workspace.numel(), pe,
+           _raw_stream(stream, dev)), "sa_prompt_attention")
     return o_out, lse_out
+
+
+_NO_QUERIES = (ctypes.c_int64 * 3)(0, 0, 1)
 
 
 def _append_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page_map, seq_lens,
                  summaries, interleaved, q_out, k_out, out_seq_lens, dev_error, stream):
-    lib = load()
-    if k_new.dim() != 3 or k_new.dtype is not torch.bfloat16:
-        raise TypeError("k_new must be a bfloat16 tensor [tokens, Hkv, D]")
-    total, Hkv, D = k_new.shape
-    _packed(v_new, Hkv, D, "v_new")
-    if v_new.shape[0] != total:
-        raise ValueError("k_new and v_new must hold the same tokens")
-    B = _batch_of(cu_new, "cu_new")
-    _dense(seq_lens, torch.int32, (B,), "seq_lens")
-    P_pool, heads, P, _ = _cache_pair(k_cache, v_cache, D)
-    if heads != Hkv:
-        raise ValueError("the caches must have k_new's heads")
-    n_pos = rot = 0
+    lib = _lib or load()
+    kshape = total, Hkv, D = _rank(k_new, 3, "k_new")
+    cshape = P_pool, _, P, _ = _rank(k_cache, 4, "k_cache")
+    B = _offsets(cu_new, "cu_new")
+    n_map = _map_of(page_map, B)
+    if not (v_new.dtype is _BF16 and v_new.shape == kshape and v_cache.dtype is _BF16
+            and v_cache.shape == cshape and cshape[1] == Hkv and cshape[3] == D
+            and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()):
+        _like(v_new, _BF16, kshape, "v_new", contiguous=False)
+        _like(k_cache, _BF16, (P_pool, Hkv, P, D), "k_cache", contiguous=False)
+        _like(v_cache, _BF16, cshape, "v_cache", contiguous=False)
+        _like(seq_lens, _I32, (B,), "seq_lens")
+    n_pos = rot = Hq = 0
+    qs = _NO_QUERIES
     if rope_table is not None:
-        if rope_table.dtype is not torch.float32 or rope_table.dim() != 2 or \
+        if rope_table.dtype is not _F32 or rope_table.dim() != 2 or \
                 not rope_table.is_contiguous():
             raise TypeError("rope_table must be a contiguous float32 tensor [positions, rot_dim]")
         n_pos, rot = rope_table.shape
-    Hq = 0
-    qs = (0, 0, 1)
     if q_new is not None:
-        if q_new.dim() != 3 or q_new.shape[0] != total:
-            raise ValueError("q_new must hold k_new's tokens")
-        Hq = q_new.shape[1]
-        _packed(q_new, Hq, D, "q_new")
-        qs = q_new.stride()
+        qshape = _, Hq, _ = _rank(q_new, 3, "q_new")
+        if qshape[0] != total or qshape[2] != D:
+            raise ValueError("q_new must hold k_new's tokens and features")
+        qs = _stride_array(q_new)
         if q_out is None:
-            q_out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=q_new.device)
-        else:
-            _dense(q_out, torch.bfloat16, (total, Hq, D), "q_out")
+            q_out = torch.empty(qshape, dtype=_BF16, device=q_new.device)
+        elif not (q_out.dtype is _BF16 and q_out.shape == qshape and q_out.is_contiguous()):
+            _like(q_out, _BF16, qshape, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q_new")
     if k_out is not None:
-        _dense(k_out, torch.bfloat16, (total, Hkv, D), "k_out")
-    if summaries is not None:
-        _dense(summaries, torch.bfloat16, (P_pool, Hkv, D), "summaries")
-    if out_seq_lens is not None:
-        _dense(out_seq_lens, torch.int32, (B,), "out_seq_lens")
-    _error_word(dev_error)
+        _like(k_out, _BF16, kshape, "k_out")
+    if summaries is not None and not (summaries.dtype is _BF16 and summaries.is_contiguous()
+                                      and summaries.shape == (P_pool, Hkv, D)):
+        _like(summaries, _BF16, (P_pool, Hkv, D), "summaries")
+    if out_seq_lens is not None and not (out_seq_lens.dtype is _I32 and out_seq_lens.shape == (B,)
+                                         and out_seq_lens.is_contiguous()):
+        _like(out_seq_lens, _I32, (B,), "out_seq_lens")
+    if dev_error is not None and dev_error.dtype is not _I32:
+        raise TypeError("dev_error must be an int32 tensor")
     dev = k_new.get_device()
-    if len(page_map) == 1:
-        name, fn, blocks = "sa_append_kv_rope", lib.sa_append_kv_rope, None
-        n_map = _page_table(page_map[0], B)
+    flat = len(page_map) == 1
+    pq, pk, pv, pcu, pt, pqo, pko, pkc, pvc, pm, pb, psl, pnl, psig, pe = _ptrs(
+        dev, q_new, k_new, v_new, cu_new, rope_table, q_out, k_out, k_cache, v_cache, page_map[0],
+        None if flat else page_map[1], seq_lens, out_seq_lens, summaries, dev_error)
+    head = (pq, qs, pk, _stride_array(k_new), pv, _stride_array(v_new), pcu, total, pt, n_pos, rot,
+            1 if interleaved else 0, pqo, pko, pkc, _stride_array(k_cache), pvc,
+            _stride_array(v_cache), pm, n_map)
+    rest = (psl, pnl, B, Hq, Hkv, D, P, P_pool, psig, pe, _raw_stream(stream, dev))
+    if flat:
+        _call(lib.sa_append_kv_rope, head + rest, "sa_append_kv_rope")
     else:
-        name, fn, blocks = "sa_append_kv_rope_dir", lib.sa_append_kv_rope_dir, page_map[1]
-        _page_dir(*page_map, B)
-    pq, pk, pv, pcu, pt, pqo, pko, pkc, pvc, pmap, pb, psl, pnl, psig, pe = _ptrs(
-        (q_new, k_new, v_new, cu_new, rope_table, q_out, k_out, k_cache, v_cache, page_map[0],
-         blocks, seq_lens, out_seq_lens, summaries, dev_error), dev)
-    margs = (pmap, n_map) if blocks is None else (pmap, page_map[0].shape[1], pb,
-                                                  blocks.shape[0], page_map[2])
-    _call(fn, (pq, _stride_array(qs), pk, _stride_array(k_new.stride()), pv,
-               _stride_array(v_new.stride()), pcu, total, pt, n_pos, rot, 1 if interleaved else 0,
-               pqo, pko, pkc, _stride_array(k_cache.stride()), pvc,
-               _stride_array(v_cache.stride()), *margs, psl, pnl, B, Hq, Hkv, D, P, P_pool, psig,
-               pe, _raw_stream(stream, dev)), name)
+        _call(lib.sa_append_kv_rope_dir, head + (pb, page_map[1].shape[0], page_map[2]) + rest,
+              "sa_append_kv_rope_dir")
     return q_out, out_seq_lens
 
 
