@@ -406,3 +406,60 @@ def test_prompt_under_load(B, lo, hi, G, Hkv, D, window):
     for _ in range(3):
         o, lse = sa.sa_prompt_attention(q, k, v, cu, cu, 1.0 / math.sqrt(D), window=window)
         check64(o, lse, q, ks, vs, ns, 1.0 / math.sqrt(D), window)
+
+
+def test_prompt_over_views_of_one_projection():
+    # q, k, v as slices of a fused [tokens, (Hq + 2 Hkv), D] projection: no copies
+    g = torch.Generator().manual_seed(4)
+    ns, G, Hkv, D = [300, 45], 4, 2, 128
+    qkv = _randn(g, sum(ns), (G + 2) * Hkv, D)
+    q, k, v = qkv[:, :G * Hkv], qkv[:, G * Hkv:(G + 1) * Hkv], qkv[:, (G + 1) * Hkv:]
+    cu = _cu(ns)
+    o, lse = sa.sa_prompt_attention(q, k, v, cu, cu, 0.08)
+    check64(o, lse, q, torch.split(k, ns), torch.split(v, ns), ns, 0.08, 0)
+
+
+def test_non_finite_scores_stay_in_their_rows():
+    # a query of inf and one of NaN give NaN rows; every other row is as without them
+    c = chunk_case(21, [3, 40], [300, 700], 4, 2, 128, 16)
+    o, lse, _ = run_chunk(c)
+    c["q"][1, 2] = float("inf")
+    c["q"][20, 5] = float("nan")
+    o2, lse2, err = run_chunk(c)
+    assert err == 0
+    keep = torch.ones(o.shape[:2], dtype=torch.bool, device=DEV)
+    keep[1, 2] = keep[20, 5] = False
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert bool(o2[1, 2].isnan().all()) and bool(o2[20, 5].isnan().all()) and bool(lse2[20, 5].isnan())
+
+
+def test_recorded_call_is_the_call():
+    c = chunk_case(22, [1, 9], [400, 90], 4, 2, 64, 16)
+    want, want_lse, _ = run_chunk(c)
+    ws = sa.dense_attention_workspace(10, 8, 2, 64, DEV)
+    o, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    run = sa.bind(lambda: sa.sa_chunk_attention(c["q"], c["kc"], c["vc"], c["pt"], c["sl"], c["cu"], c["scale"],
+                                                o_out=o, lse_out=lse, workspace=ws))
+    assert run.n_calls == 1
+    run()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def test_python_refuses_what_the_call_would_misread():
+    c = chunk_case(23, [2], [40], 4, 2, 64, 16)
+    args = lambda **kw: {**dict(q=c["q"], k_cache=c["kc"], v_cache=c["vc"], page_table=c["pt"], seq_lens=c["sl"],  # noqa: E731
+                                cu_q=c["cu"], scale=0.1), **kw}
+    for bad in (dict(seq_lens=c["sl"].long()), dict(cu_q=c["cu"].float()), dict(v_cache=c["vc"][:, :1]),
+                dict(page_table=c["pt"].repeat(2, 1)), dict(o_out=torch.empty_like(c["q"])[:, :4]),
+                dict(lse_out=torch.empty((2, 7), device=DEV)), dict(k_cache=c["kc"].float()),
+                dict(workspace=torch.empty(100, device=DEV)), dict(seq_lens=c["sl"].repeat(2))):
+        with pytest.raises((TypeError, ValueError)):
+            sa.sa_chunk_attention(**args(**bad))
+    for bad in (dict(seq_lens=c["sl"].cpu()), dict(k_cache=c["kc"].cpu(), v_cache=c["vc"].cpu())):
+        with pytest.raises(ValueError):
+            sa.sa_chunk_attention(**args(**bad))
+    with pytest.raises(sa.SAError):
+        sa.sa_chunk_attention(**args(scale=-1.0))
+    with pytest.raises(sa.SAError):
+        sa.sa_chunk_attention(**args(workspace=torch.empty(100, dtype=torch.uint8, device=DEV)))

@@ -246,3 +246,57 @@ def test_a_serving_loop():
     torch.cuda.synchronize()
     assert float((out[4].view(3, Hq) - lse).abs().max()) < 1e-4
     check(o, lse, q, ks, vs, [1, 1, 1], scale, 0)
+
+
+def test_append_of_nothing_reports_the_lengths():
+    c = _case(36, [0, 0], [5, 20], 4, 2, 64, 16, 64)
+    d = _gpu(c)
+    before = [d[x].clone() for x in ("kc", "vc", "sig")]
+    _, new, err = _run(d)
+    assert err == 0 and np.array_equal(new.cpu().numpy(), [5, 20])
+    for a, b in zip(before, (d["kc"], d["vc"], d["sig"])):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_a_captured_serving_step():
+    # append, attend and move the lengths on, captured once and replayed token by token:
+    # the cache, the lengths and the last answer are those of the same calls made one by one
+    Hq, Hkv, D, P, B, n = 8, 2, 128, 16, 3, 20
+    c = _case(42, [n] * B, [3, 30, 700], Hq, Hkv, D, P, 128)
+    g = torch.Generator().manual_seed(5)
+    feed = [[torch.randn((B, h, D), generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, Hkv, Hkv)] for _ in range(n)]
+    cu = _i32([0, 1, 2, 3])
+    ws = sa.dense_attention_workspace(B, Hq, Hkv, D, DEV)
+
+    def step(d, x, lens, new, qo, o, lse):
+        sa.sa_append_kv_rope(x[0], x[1], x[2], cu, d["table"], d["kc"], d["vc"], d["pt"], lens, d["sig"], q_out=qo,
+                             out_seq_lens=new)
+        sa.sa_chunk_attention(qo, d["kc"], d["vc"], d["pt"], new, cu, 0.09, o_out=o, lse_out=lse, workspace=ws)
+        lens.copy_(new)
+
+    ends = []
+    for captured in (False, True):
+        d = _gpu(c)
+        x = [t.clone() for t in feed[0]]
+        lens, new = d["sl"].clone(), torch.empty_like(d["sl"])
+        qo, o, lse = torch.empty_like(x[0]), torch.empty_like(x[0]), torch.empty((B, Hq), device=DEV)
+        if captured:
+            step(d, x, lens, new, qo, o, lse)     # warm-up, on a copy of the state
+            d, lens = _gpu(c), lens
+            lens.copy_(d["sl"])
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step(d, x, lens, new, qo, o, lse)
+        for y in feed:
+            for a, b in zip(x, y):
+                a.copy_(b)
+            if captured:
+                graph.replay()
+            else:
+                step(d, x, lens, new, qo, o, lse)
+        torch.cuda.synchronize()
+        ends.append([t.clone() for t in (d["kc"], d["vc"], d["sig"], lens, o, lse)])
+    for a, b in zip(*ends):
+        assert torch.equal(a.view(torch.int16) if a.dtype == torch.bfloat16 else a,
+                           b.view(torch.int16) if b.dtype == torch.bfloat16 else b)
