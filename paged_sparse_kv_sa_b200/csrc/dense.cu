@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // part, the others the continuing parts of the CTAs after it.  Most cut items have
 // two parts: both parts' loads of all rows are in flight together.
 template <int D, int R>
-__global__ void __launch_bounds__(1024) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
+__global__ void __launch_bounds__(512) dense_merge_kernel(const __grid_constant__ DenseArgs a) {
   pdl_wait_and_release();
   const int32_t* h = a.part_head + blockIdx.x * 8;
   const int4 h0 = *reinterpret_cast<const int4*>(h);
@@ -967,8 +967,9 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensor
   dense_kernel<D><<<ctas, kThreads, Cfg<D>::kDyn, stream>>>(a, qmap, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // the merge is launched under the first kernel's tail (it waits for its end);
-  // few rows: one per warp, in one block per item; many: four per warp
+  // the merge is launched under the first kernel's tail (it waits for its end); a
+  // warp does one row where rows are few, two where they are many (four, in blocks
+  // of 32 warps: 16 x 32K-key decode 358 us, so 354)
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -976,14 +977,14 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensor
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  if (a.rows_cap <= 16) {
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(32 * a.rows_cap);
+  if (a.rows_cap <= 64) {
+    cfg.gridDim = dim3(ctas, (a.rows_cap + 15) / 16);
+    cfg.blockDim = dim3(32 * (a.rows_cap < 16 ? a.rows_cap : 16));
     return cudaLaunchKernelEx(&cfg, dense_merge_kernel<D, 1>, a);
   }
-  cfg.gridDim = dim3(ctas, (a.rows_cap + 127) / 128);
-  cfg.blockDim = dim3(1024);
-  return cudaLaunchKernelEx(&cfg, dense_merge_kernel<D, 4>, a);
+  cfg.gridDim = dim3(ctas, (a.rows_cap + 31) / 32);
+  cfg.blockDim = dim3(512);
+  return cudaLaunchKernelEx(&cfg, dense_merge_kernel<D, 2>, a);
 }
 
 int rows_cap_of(int total_q, int Hq, int Hkv) {
