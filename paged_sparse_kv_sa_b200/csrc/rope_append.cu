@@ -13,17 +13,19 @@
 //
 // Two kinds of CTA share the launch.  A page CTA owns some kv heads of a touched
 // page (as many as its stage holds when there are pages enough to fill the GPU,
-// so that their loads share one chain of look-ups; one otherwise): it reads the page's old keys and rotates and writes the new ones in
-// 16-byte pieces (both halves of a rotated pair in one thread), leaves them in
-// shared memory as well, and then sums each column in float64 from there (one
-// column per thread: few registers, so enough CTAs are resident to keep the
-// loads in flight; the sums kept per thread while loading took 109 us where
-// this takes 43 us for 8254 tokens).  A query CTA rotates the heads of a few
-// tokens, one warp per token: a lane keeps its unit of the head, so it reads its
-// cosines and sines once for all heads.  Page slots and tokens find their sequence by a 32-way search
-// of the offsets: slot s belongs to the last b with floor(cu[b]/P) + 2b <= s
-// (n tokens touch at most floor(n/P) + 2 pages), so the grid needs only the
-// packed total.  Memory-bound: every byte is moved once.
+// so that their loads share one chain of look-ups; one otherwise): it reads the
+// page's old keys and rotates and writes the new ones in 16-byte pieces (both
+// halves of a rotated pair in one thread), leaves them in shared memory as well,
+// and then sums each column in float64 from there (one column per thread: few
+// registers, so enough CTAs are resident to keep the loads in flight; 8254 tokens
+// with the sums kept per thread while loading 109 us, with one column per thread
+// 65, with several heads per CTA 45, with two heads in flight 41; 208 MB, so 5.1
+// TB/s).  A query CTA rotates the heads of a few tokens, one warp per token: a
+// lane keeps its unit of the head, so it reads its cosines and sines once for all
+// heads.  Page slots and tokens find their sequence by a 32-way search of the
+// offsets: slot s belongs to the last b with floor(cu[b]/P) + 2b <= s (n tokens
+// touch at most floor(n/P) + 2 pages), so the grid needs only the packed total.
+// Memory-bound: every byte is moved once.
 //
 // Sources: "Universal Attention Engine — Declarative Sparse Attention for
 // Production", "Architecture" (a PagedAttention-compatible cache) and

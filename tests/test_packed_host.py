@@ -145,9 +145,13 @@ def test_oracle_rotated_scores_depend_on_distance_alone():
     q, k = (np.repeat(_bits(rng.standard_normal((1, 1, 64))), 50, 0) for _ in range(2))
     rq, rk = (O.bf16_to_f64(O.rotate_bf16(x, table, np.arange(50)))[:, 0] for x in (q, k))
     s = rq @ rk.T
+    # each rotated feature is off by at most 2^-8 of itself (its rounding to bf16; the
+    # table's and the float32 steps' 2^-21 lie inside the 2.1), a pair's products sum to
+    # at most |q pair| |k pair| in magnitude at every position, and two scores differ
+    pair = lambda x: np.hypot(*np.split(O.bf16_to_f64(x[0, 0]), 2))
+    tol = 2 * 2.1 * 2.0 ** -8 * pair(q) @ pair(k)
     for d in range(0, 40, 7):
-        diag = np.diagonal(s, d)
-        assert np.ptp(diag) <= 2 * 2.0 ** -8 * 2 * np.abs(rq[0]) @ np.abs(rk[0]) + 0.2
+        assert np.ptp(np.diagonal(s, d)) <= tol
 
 
 @pytest.mark.parametrize("n,L,window", [(1, 7, 0), (5, 5, 0), (4, 30, 9), (6, 3, 0), (3, 20, 1)])
