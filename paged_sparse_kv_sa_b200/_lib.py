@@ -883,6 +883,16 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to the stream of the call: one made on the current stream
+    could be memory that stream still uses, or be handed out again by it, while the call
+    runs on another."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _like(t, dtype, shape, what, contiguous=True):
     """Raise unless t (None: passes) has this type and shape, and is contiguous."""
     if t is None:
@@ -920,20 +930,24 @@ def _map_of(page_map, B):
 def dense_attention_workspace(total_q: int, Hq: int, Hkv: int, D: int, device):
     """A workspace for sa_chunk_attention(_dir) and sa_prompt_attention (reusable by
     calls that do not overlap; large enough for any call of at most total_q tokens)."""
+    return _dense_workspace(total_q, Hq, Hkv, D, device, None)
+
+
+def _dense_workspace(total_q, Hq, Hkv, D, device, stream):
     n = int(load().sa_dense_attention_workspace_size(total_q, Hq, Hkv, D))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return _empty(max(n, 16), torch.uint8, device, stream)
 
 
-def _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace, dev_error):
+def _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace, dev_error, stream):
     """The outputs and workspace of a dense call, made where they are not given."""
     if not q.is_cuda:
         raise ValueError("tensors must be on the current GPU")
     if o_out is None:
-        o_out = torch.empty(shape, dtype=_BF16, device=q.device)
+        o_out = _empty(shape, _BF16, q.device, stream)
     if lse_out is None:
-        lse_out = torch.empty(shape[:2], dtype=_F32, device=q.device)
+        lse_out = _empty(shape[:2], _F32, q.device, stream)
     if workspace is None:
-        workspace = dense_attention_workspace(shape[0], shape[1], Hkv, shape[2], q.device)
+        workspace = _dense_workspace(shape[0], shape[1], Hkv, shape[2], q.device, stream)
     _like(o_out, _BF16, shape, "o_out")
     _like(lse_out, _F32, shape[:2], "lse_out")
     _like(workspace, torch.uint8, workspace.shape, "workspace")
@@ -965,7 +979,7 @@ def _chunk(q, k_cache, v_cache, page_map, seq_lens, cu_q, scale, window, o_out, 
         _like(seq_lens, _I32, (B,), "seq_lens")
     if not _dense_fine(shape, o_out, lse_out, workspace, dev_error):
         o_out, lse_out, workspace = _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace,
-                                                   dev_error)
+                                                   dev_error, stream)
     dev = q.get_device()
     flat = len(page_map) == 1
     pq, pcu, pk, pv, pm, pb, psl, po, pl, pw, pe = _ptrs(
@@ -1019,7 +1033,7 @@ def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_ou
         _like(cu_k, _I32, (B + 1,), "cu_k")
     if not _dense_fine(shape, o_out, lse_out, workspace, dev_error):
         o_out, lse_out, workspace = _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace,
-                                                   dev_error)
+                                                   dev_error, stream)
     dev = q.get_device()
     pq, pcu, pk, pv, pck, po, pl, pw, pe = _ptrs(dev, q, cu_q, k, v, cu_k, o_out, lse_out,
                                                  workspace, dev_error)
@@ -1060,7 +1074,7 @@ def _append_rope(q_new, k_new, v_new, cu_new, rope_table, k_cache, v_cache, page
             raise ValueError("q_new must hold k_new's tokens and features")
         qs = _stride_array(q_new)
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=_BF16, device=q_new.device)
+            q_out = _empty(qshape, _BF16, q_new.device, stream)
         elif not (q_out.dtype is _BF16 and q_out.shape == qshape and q_out.is_contiguous()):
             _like(q_out, _BF16, qshape, "q_out")
     elif q_out is not None:

@@ -332,6 +332,21 @@ def test_two_streams_with_their_own_workspaces():
         assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
+def test_tensors_made_by_the_call_belong_to_its_stream():
+    c = chunk_case(19, [1, 20], [3000, 800], 4, 2, 128, 16)
+    want = run_chunk(c)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)   # some 25 ms: the call waits behind it
+    o, lse = sa.sa_chunk_attention(c["q"], c["kc"], c["vc"], c["pt"], c["sl"], c["cu"], c["scale"], stream=s)
+    n = sa.dense_attention_workspace(21, 8, 2, 128, DEV).numel()
+    for x in [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(4)]:   # the workspace's memory, were it free
+        x.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 # ------------------------------------------------------------------ loads that fill the GPU
 def dense64(q, k, v, scale, window):
     """O.dense_attention for one sequence, in float64 torch operations on the GPU."""
