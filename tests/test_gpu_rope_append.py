@@ -182,6 +182,29 @@ def test_bad_pages_lengths_and_offsets_are_flagged_and_skipped():
         assert err & flag
 
 
+@pytest.mark.parametrize("cu,skipped", [([-5, 20, 23], (0, 20)), ([0, 20, 5000], (20, 23)), ([0, -1, 23], None)])
+def test_a_sequence_with_bad_offsets_is_skipped(cu, skipped):
+    c = _case(35, [20, 3], [0, 5], 4, 2, 64, 16, 64)
+    d = dict(_gpu(c), cu=_i32(cu))
+    before = {k: d[k].clone() for k in ("kc", "vc", "sig")}
+    qo = torch.full_like(d["q"], 7.0)
+    qo, _, err = _run(d, q_out=qo)
+    assert err & 4
+    if skipped is None:   # offsets that turn back: neither sequence holds
+        assert all(torch.equal(d[k], x) for k, x in before.items())
+        return
+    x, y = skipped
+    assert bool((qo[x:y] == 7).all())
+    other = 1 if x == 0 else 0
+    rest = slice(20, 23) if other else slice(0, 20)
+    q, _, kc, vc, sig, _ = _want(c)
+    assert np.array_equal(_bits(qo)[rest], q[rest])
+    mine = c["pt"][other][:-(-(len(range(*rest.indices(23))) + int(c["sl"][other])) // 16)]
+    pages = np.setdiff1d(np.arange(kc.shape[0]), mine)
+    assert np.array_equal(_bits(d["kc"])[mine], kc[mine]) and np.array_equal(_bits(d["sig"])[mine], sig[mine])
+    assert all(np.array_equal(_bits(d[k])[pages], _bits(b)[pages]) for k, b in before.items())
+
+
 def test_two_level_map_is_the_flat_call():
     c = _case(35, [40, 3], [100, 250], 8, 2, 128, 16, 128, spare=3)
     d, e = _gpu(c), _gpu(c)
