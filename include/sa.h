@@ -623,7 +623,8 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  * of tokens the call is given.  Tokens behind cu[B] are neither read nor
  * written.  An offset that breaks this is flagged (SA_DEVERR_COUNT): the
  * attention calls then hold it inside the tensors (what such a sequence's rows
- * receive is unspecified), the append skips the sequence.
+ * receive is unspecified; where offsets turn back, so that sequences share
+ * tokens, what any row receives, if anything), the append skips the sequence.
  * Strides are three (token, head, feature), with the rules of every bf16
  * tensor (feature 1, the others multiples of 8, base 16-byte aligned).
  */

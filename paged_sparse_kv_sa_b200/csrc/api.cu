@@ -1245,7 +1245,8 @@ bool dense_countable(const DenseArgs& a, int64_t max_len) {
   const int64_t toks = 2 * a.tile_toks;
   const int64_t keys = a.window && a.window + toks < max_len ? a.window + toks : max_len;
   const int64_t items = a.total_q / toks + a.B;
-  return items * (keys / 128 + 3) < 0x7fffffffLL / a.Hkv;
+  // an item's fixed two, and its tiles: a window's may start and end inside one
+  return items * (keys / 128 + 4) < 0x7fffffffLL / a.Hkv;
 }
 
 // What the dense attention calls share: sizes, outputs, workspace.
