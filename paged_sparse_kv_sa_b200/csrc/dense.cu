@@ -737,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- this CTA's share [w_pos, w_hi) of all units, and the item it starts in.
       // Shares of w_share or w_share + 1 units, the first w_extra of them the longer.
       // The units of sequences that share no tokens are fewer than 2^31 (checked on
-      // the host); offsets that turn back can give more, and then nothing is planned.
+      // the host); offsets that turn back (and are flagged) can give more, and then
+      // nothing is planned.
       // The sum in 64 bits, the lanes' high and low parts added apart (each lane holds
       // at most 128 sequences of fewer than 2^31).
       int64_t w_sum = 0;
@@ -746,7 +747,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                << 16) +
               __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w_sum & 0xffff));
       const bool countable = w_sum <= 0x7fffffff / a.Hkv;
-      if (!countable && cta == 0 && lane == 0) set_dev_error(a.err, SA_DEVERR_COUNT);
       const int w_total = countable ? static_cast<int>(w_sum) * a.Hkv : 0;
       const int n_eff = min(n_ctas, max(1, w_total / kMinUnits));
       const int w_share = w_total / n_eff, w_extra = w_total - w_share * n_eff;
