@@ -128,13 +128,20 @@ struct Seg {
 // false: gave up.  The result is meant to be kept and looked at once a tile, not
 // branched on here: a vote or a branch at every wait made the tensor core's
 // issuing warp, and with it every tile, slower (8192-token prompt 535 -> 516 us,
-// packed short prompts 244 -> 213 us without).
+// packed short prompts 244 -> 213 us without), and so did raising the CTA's flag
+// from here (packed prompts 187 -> 198 us).
+#ifdef SA_DENSE_POLLS   // a build whose waits run out early: a test of the way out
+#define SA_DENSE_TRY "test_wait"
+constexpr uint32_t kPolls = SA_DENSE_POLLS;
+#else
+#define SA_DENSE_TRY "try_wait"
 constexpr uint32_t kPolls = 1u << 17;
+#endif
 SA_DEV bool wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-      "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "W:\n mbarrier." SA_DENSE_TRY ".parity.shared::cta.b64 p, [%1], %2;\n"
       " @p bra D;\n add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra W;\n"
       "D:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
@@ -142,12 +149,17 @@ SA_DEV bool wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Whether no lane of the warp has given up; a warp that has raises the CTA's flag,
-// and every warp that sees it goes on without waiting.
+// Whether no lane of the warp has given up; a warp that has raises the CTA's flag:
+// the loaders then ask for nothing more, and the others' waits run out.
 SA_DEV bool all_well(bool ok, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, ok)) return true;
   *abort_flag = 1;
   return false;
+}
+// Phase `parity` of `bar`, at most 2^16 polls, whatever the CTA's flag says: the copies
+// and products in flight of a CTA that has given up.
+SA_DEV void drain(uint64_t* bar, uint32_t parity) {
+  for (uint32_t n = 0; n < 1u << 16 && !mbar_try_wait(bar, parity); ++n) {}
 }
 // All threads of the CTA, from whichever role's code they are in.
 SA_DEV void cta_sync() { asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory"); }
@@ -246,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* v_s = k_s + C::kStages * C::kTileBytes;
   __shared__ uint64_t k_full[C::kStages], k_empty[C::kStages];
   __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages], v_tail[C::kStages];
-  __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty;
+  __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty, all_done;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, n_segs_s, last_s;
   __shared__ Seg seg_s[kMaxSegs];
@@ -276,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
+    mbar_init(&all_done, 1);
     abort_s = 0;
     fence_mbar_init();
     a.part_head[cta * 8] = 0;   // no part of this CTA starts an item, so far
@@ -543,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (halves) pair_sync(id);   // both accumulators read: the next item may write them
         kc += nt;
       }
-      if (!ok && lane == 0) set_dev_error(a.err, SA_DEVERR_TIMEOUT);
       cta_sync();
     }
   } else {
@@ -556,13 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         last = last_s;
         for (int i = 0; i < n_segs && ok; ++i) {
           const Seg s = seg_s[i];
-          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc) {
+          for (int j = s.j0; j < s.j1; ++j, ++kc) {
             const Box x = box_of(a, s, j, lane);
             if (lane == 0) {
               bad_s[kc % kBadRing] = x.bad;
               if (x.bad) set_dev_error(a.err, SA_DEVERR_POOL_RANGE);
             }
             ok = load_tile<D>(x, s.kvh, kc, k_s, &kmap, k_full, k_empty, a.box, abort_flag);
+            if (!ok) break;   // kc: the tiles asked for
           }
         }
         cta_sync();
@@ -660,8 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::mma_bf16_lo(tmem_u + 128 * w, qd + o, kd + o, C::kIdQK, kk > 0 ? 1u : 0u);
             }
             tc::commit(&s_full[w]);
-            if (halves || w == 1) tc::commit(&k_empty[st]);
-            if (qk_left == 1) tc::commit(&q_empty);
+            // (what may still be on its way frees no stage)
+            if (ok && (halves || w == 1)) tc::commit(&k_empty[st]);
+            if (ok && qk_left == 1) tc::commit(&q_empty);
           }
           __syncwarp();
           --qk_left;
@@ -694,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      vd + kk * (2048 >> 4), C::kIdPV,
                                      (it > 0 || kk > 0) ? 1u : 0u);
               if (h == 1) {
-                if (halves || w == 1) tc::commit(&v_empty[st]);
+                if (ok && (halves || w == 1)) tc::commit(&v_empty[st]);
                 if (it + 1 == (w ? n_b : n_a)) tc::commit(&o_done[w]);
               }
             }
@@ -730,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           kc += nt;
           ++qc;
         }
+        all_well(ok, abort_flag);
         cta_sync();
       }
     } else if (warp == kPlanWarp) {
@@ -847,10 +862,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = s.j0; j < s.j1 && ok; ++j, ++kc) {
             ok = load_tile<D>(box_of(a, s, j, lane), s.kvh, kc, v_s, &vmap, v_full, v_empty, a.box,
                               abort_flag);
+            if (!ok) break;
             // Value rows past the sequence's end may hold anything (0 * NaN): zeroed,
             // up to the 16-key step that is multiplied (only in an item's last tile).
             const int z0 = s.L - j * kKeys, nz = 16 * min(8, (hi - j * kKeys + 15) / 16) - z0;
-            if (nz > 0 && ok) {
+            if (nz > 0) {
               const int st = kc % C::kStages;
               ok = all_well(wait(&v_full[st], (kc / C::kStages) & 1), abort_flag);
               uint8_t* vt = v_s + st * C::kTileBytes + z0 * 128;
@@ -868,13 +884,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       } while (!last);
     }
   }
-  if ((warp == kLoadWarp || warp == kPlanWarp) && abort_s) {
-    // leave only when no copy of this CTA is in flight any more (the last wait
-    // of a tile that was never asked for runs out)
-    uint64_t* full = warp == kLoadWarp ? k_full : v_full;
-    for (uint32_t c = kc > (uint32_t)C::kStages ? kc - C::kStages : 0; c < kc; ++c)
-      for (uint32_t n = 0; n < 1u << 16 && !mbar_try_wait(&full[c % C::kStages],
-                                                        (c / C::kStages) & 1); ++n) {}
+  // (every role has passed its last barrier: no wait is left that could raise the flag)
+  if (abort_s) {
+    // leave only when no copy and no product of this CTA is in flight any more
+    if (warp == kLoadWarp || warp == kPlanWarp) {
+      uint64_t* full = warp == kLoadWarp ? k_full : v_full;
+      for (uint32_t c = kc > (uint32_t)C::kStages ? kc - C::kStages : 0; c < kc; ++c)
+        drain(&full[c % C::kStages], (c / C::kStages) & 1);
+    } else if (warp == kQWarp) {
+      if (qc > 0) drain(&q_full, (qc - 1) & 1);
+    } else if (warp == kMmaWarp) {
+      if (tc::elect_one()) tc::commit(&all_done);
+      __syncwarp();
+      drain(&all_done, 0);
+    }
+    if (tid == 0) set_dev_error(a.err, SA_DEVERR_TIMEOUT);
   }
   tc::fence_before_sync();
   __syncthreads();
