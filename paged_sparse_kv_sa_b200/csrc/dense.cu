@@ -69,11 +69,14 @@ struct Cfg {
   static constexpr int kQBytes = kM * D * 2;
   static constexpr int kTileBytes = kKeys * D * 2;
   static constexpr int kStages = D == 64 ? 4 : 2;
+  // A tile's missing boxes are noted before its stage is waited for, when the tensor
+  // core is known to have read the keys of tile c - 1 - kStages; the softmax of that
+  // tile, and of the one before (the other half's), may still have to look theirs up.
+  static_assert(kBadRing >= kStages + 3, "tiles whose missing boxes are still looked up");
   static constexpr int kDyn = 2 * kQBytes + 2 * kStages * kTileBytes + 1024;
   static constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kM, kKeys, false, false);
   static constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kM, D, false, true);
 };
-static_assert(kBadRing > 4, "more tiles than a ring and its consumers hold");
 
 // ---------------------------------------------------------------- geometry
 struct Seq {
