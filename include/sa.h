@@ -661,8 +661,9 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  *  out_seq_lens (dev, optional) [B] int32: receives seq_lens[b] + n_b; must not
  *             be seq_lens itself
  *  summaries  (dev, optional) [P_pool,Hkv,D] bf16, contiguous
- * D % 8 == 0, D <= 256; rot_dim % 16 == 0, rot_dim <= D.  Appends that touch
- * the same page from two sequences race.
+ * D % 8 == 0, D <= 256; rot_dim % 16 == 0, rot_dim <= D; max_pages * page_size
+ * + total_new and page_size * D below 2^31 (SA_ERR_UNSUPPORTED otherwise).
+ * Appends that touch the same page from two sequences race.
  */
 SA_API int sa_append_kv_rope(const uint16_t* q_new, const int64_t q_strides[3],
                              const uint16_t* k_new, const int64_t kn_strides[3],

@@ -1203,7 +1203,10 @@ int rope_append_impl(const uint16_t* q, const int64_t* qs, const uint16_t* k, co
   if (int r = check_cache(v_cache, vs)) return r;
   if (!pm.table || (rot > 0 && (!table || !aligned16(table))) || (k_out && !aligned16(k_out)))
     return SA_ERR_INVALID_ARG;
-  if (D > 256 || (int64_t)max_pages * page_size > 0x7fffffffLL - total) return SA_ERR_UNSUPPORTED;
+  // (the kernel indexes a page's elements in 32 bits)
+  if (D > 256 || (int64_t)max_pages * page_size > 0x7fffffffLL - total ||
+      (int64_t)page_size * D > 0x7fffffffLL)
+    return SA_ERR_UNSUPPORTED;
   RopeAppendArgs a = {};
   a.q = q;
   if (q && qs) a.q0 = qs[0], a.q1 = qs[1];
