@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (moved) break;
             // (a NaN score makes the row's maximum, and so the row, NaN)
             const float mx = max_nan(max64(x, 0), max64(x, 64)) * sl;
-            const bool move = !(mx <= m_ref + kLazy);
+            // (only rows that are kept: the others hold whatever their queries' memory does)
+            const bool move = row_ok && !(mx <= m_ref + kLazy);
             if (!__any_sync(0xffffffffu, move)) break;
             const float alpha = move ? exp2f(m_ref - mx) : 1.f;
             m_new = move ? mx : m_ref;

@@ -1,7 +1,6 @@
-"""Edges of the packed-batch operators (marked gpu): batches whose offsets turn back."""
-import torch
-
+"""Edges of the packed-batch operators (marked gpu)."""
 import pytest
+import torch
 
 import paged_sparse_kv_sa_b200 as sa
 from test_gpu_dense import check, chunk_case, run_chunk
@@ -28,3 +27,16 @@ def test_offsets_that_turn_back_do_not_pass_the_counters():
     o, lse, err = run_chunk(c, workspace=ws)
     assert err == 0
     check(o, lse, c["q"], c["ks"], c["vs"], [1, 30], c["scale"], 0)
+
+
+@pytest.mark.parametrize("ns,Ls,G,D", [([35], [3000], 7, 128), ([3], [2500], 8, 128), ([60, 2], [900, 700], 4, 64)])
+def test_queries_that_are_nobodys_change_no_bit(ns, Ls, G, D):
+    # the boxes of queries bring the tokens behind a batch along: whatever they hold, the
+    # rows that are kept are the same bits
+    c = chunk_case(81, ns, Ls, G, 2, D, 16, tail=40)
+    want = run_chunk(c)
+    for x in (float("nan"), float("inf"), 3e38):
+        c["q"][sum(ns):] = x
+        o, lse, err = run_chunk(c)
+        assert err == 0 and torch.equal(o[:sum(ns)], want[0][:sum(ns)])
+        assert torch.equal(lse[:sum(ns)], want[1][:sum(ns)])
