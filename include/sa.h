@@ -709,10 +709,13 @@ SA_API int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[
  *             16-byte aligned, caller-owned, no initial contents; calls (or
  *             captured graphs) sharing one must not overlap
  * Probabilities enter the value product as bf16 (one rounding each); sums, the
- * softmax statistics and the LSE are float32.  Keys and values past a
- * sequence's end may hold anything; the sequence's own must be finite.  Keys on
- * a page whose id is out of range are left out (SA_DEVERR_POOL_RANGE); a
- * seq_len outside the page map is held inside it (SA_DEVERR_PAGE_RANGE).
+ * softmax statistics and the LSE are float32.  Keys and values that no token of
+ * the sequence sees -- past its end, or behind the window of its first new token
+ * -- may hold anything, and the ids of pages that hold only such keys are not
+ * looked at (a serving loop may have given them back); the others must be
+ * finite.  Keys on a page whose id is out of range are left out
+ * (SA_DEVERR_POOL_RANGE); a seq_len outside the page map is held inside it
+ * (SA_DEVERR_PAGE_RANGE).
  * The result does not depend on timing: the same call gives the same bits on
  * the same kind of device.
  * Supported: D in {64,128}, page_size a multiple of 16, Hq/Hkv <= 128, B <=

@@ -33,7 +33,7 @@
 //                 box is the group's heads of as many tokens as fit 128 rows), or,
 //                 of at most 16 rows, by its own loads, the rest of the tile zero;
 //   warp 11       also plans the CTA's share first, and zeroes the value rows past
-//                 a sequence's end.
+//                 a sequence's end and behind the window.
 // An item of at most 128 rows gives both tiles the same rows and every other
 // key tile each ("halves"); the two running softmaxes merge in the epilogue,
 // both accumulators being in the same TMEM lanes.
@@ -114,6 +114,12 @@ SA_DEV int2 tiles_of(const Seq& s, int toks, int window, int qt) {
 SA_DEV int item_units(const Seq& s, int toks, int window, int qt) {
   const int2 t = tiles_of(s, toks, window, qt);
   return kItemUnits + t.y - t.x;
+}
+
+// First key that some token of a sequence of n tokens and L keys sees: those before it
+// may be anyone's.
+SA_DEV int first_key(int L, int n, int window) {
+  return window ? max(0, L - n - window + 1) : 0;
 }
 
 // A run of one item's tiles, as every role needs it.
@@ -214,7 +220,7 @@ SA_DEV Box box_of(const DenseArgs& a, const Seg& s, int j, int lane) {
   if (!a.cu_k) {
     x.page = a.P_pool;   // out of range: zeros
     x.row = 0;
-    if (key < s.L) {
+    if (key < s.L && key + a.box > first_key(s.L, s.n, a.window)) {
       const int ph = page_at(a.pt, s.b, key / a.P);
       bad = ph < 0 || ph >= a.P_pool;
       if (!bad) x.page = ph, x.row = key % a.P;
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_s = smem + 2 * C::kQBytes;
   uint8_t* v_s = k_s + C::kStages * C::kTileBytes;
   __shared__ uint64_t k_full[C::kStages], k_empty[C::kStages];
-  __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages], v_tail[C::kStages];
+  __shared__ uint64_t v_full[C::kStages], v_empty[C::kStages], v_part[C::kStages];
   __shared__ uint64_t s_full[2], p_full[2][2], o_done[2], q_full, q_empty, all_done;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s, n_segs_s, last_s;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
-      mbar_init(&v_tail[s], 32);
+      mbar_init(&v_part[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
@@ -653,9 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_desc = uni(tc::desc_lo(smem_u32(k_s), 16));
       const uint32_t v_desc = uni(tc::desc_lo(smem_u32(v_s), kKeys * 128));
       const uint32_t tmem_u = uni(tmem);
-      uint32_t tails = 0;   // bit st: phase of v_tail[st]
       // One run of an item's tiles.  halves: each row tile has every other key tile.
-      auto run = [&](int j0, int nt, int L, int hi, auto hv) {
+      auto run = [&](int j0, int nt, int hi, auto hv) {
         constexpr bool halves = decltype(hv)::value != 0;
         const int n_a = halves ? (nt + 1) / 2 : nt, n_b = halves ? nt / 2 : nt;
         int qk_left = n_a + n_b;
@@ -696,13 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = wait(&p_full[w][h], (w ? cw1 : cw0) & 1) && ok;
-            if (h == 0 && (halves || w == 0)) {
-              ok = wait(&v_full[st], (c / C::kStages) & 1) && ok;
-              if (L - j * kKeys < 16 * steps) {   // rows past the end: zeroed first
-                ok = wait(&v_tail[st], (tails >> st) & 1) && ok;
-                tails ^= 1u << st;
-              }
-            }
+            if (h == 0 && (halves || w == 0)) ok = wait(&v_full[st], (c / C::kStages) & 1) && ok;
             tc::fence_after_sync();
             if (tc::elect_one()) {
 #pragma unroll
@@ -738,13 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         last = last_s;
         for (int i = 0; i < n_segs && all_well(ok, abort_flag); ++i) {
           const Seg& s = seg_s[i];
-          const int j0 = uni(s.j0), nt = uni(s.j1) - j0, L = uni(s.L), nr = uni(s.nr);
+          const int j0 = uni(s.j0), nt = uni(s.j1) - j0, nr = uni(s.nr);
           if (nt == 0) continue;
-          const int hi = uni(min(L, L - s.n + (s.r0 + nr - 1) / G + 1));
+          const int hi = uni(min(s.L, s.L - s.n + (s.r0 + nr - 1) / G + 1));
           if (nr <= tile_rows)
-            run(j0, nt, L, hi, B);
+            run(j0, nt, hi, B);
           else
-            run(j0, nt, L, hi, A);
+            run(j0, nt, hi, A);
           kc += nt;
           ++qc;
         }
@@ -812,6 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           off -= __shfl_sync(0xffffffffu, incl, 31);
         }
       }
+      uint32_t parts = 0;           // bit st: phase of v_part[st]
+      uint64_t* part = nullptr;     // the one whose copy was given up on
       bool last = false;
       do {
         // the next segments
@@ -863,29 +864,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n_segs && ok; ++i) {   // V tiles
           const Seg s = seg_s[i];
           const int hi = min(s.L, s.L - s.n + (s.r0 + s.nr - 1) / G + 1);
-          for (int j = s.j0; j < s.j1 && ok; ++j, ++kc) {
-            ok = load_tile<D>(box_of(a, s, j, lane), s.kvh, kc, v_s, &vmap, v_full, v_empty, a.box,
-                              abort_flag);
-            if (!ok) break;
-            // Value rows past the sequence's end may hold anything (0 * NaN): zeroed,
-            // up to the 16-key step that is multiplied (only in an item's last tile).
+          const int low = first_key(s.L, s.n, a.window);
+          for (int j = s.j0; j < s.j1; ++j, ++kc) {
+            // Value rows past the sequence's end, or behind the window of its first token,
+            // may hold anything (0 * NaN).  A tile with such rows (only an item's last, up
+            // to the 16-key step that is multiplied, or its first) arrives on a barrier of
+            // its own, and on the ring's once they are zeroed: the issuing warp, whose
+            // every instruction counts, knows nothing of it (two compares a tile there:
+            // 8192-token prompt 513 -> 542 us).
+            const int st = kc % C::kStages, below = max(0, low - j * kKeys);
             const int z0 = s.L - j * kKeys, nz = 16 * min(8, (hi - j * kKeys + 15) / 16) - z0;
-            if (nz > 0) {
-              const int st = kc % C::kStages;
-              ok = all_well(wait(&v_full[st], (kc / C::kStages) & 1), abort_flag);
-              uint8_t* vt = v_s + st * C::kTileBytes + z0 * 128;
-              for (int x = lane; x < nz * 8; x += 32)
+            const bool whole = nz <= 0 && below == 0;
+            ok = load_tile<D>(box_of(a, s, j, lane), s.kvh, kc, v_s, &vmap, whole ? v_full : v_part,
+                              v_empty, a.box, abort_flag);
+            if (!ok) break;
+            if (whole) continue;
+            ok = all_well(wait(&v_part[st], (parts >> st) & 1), abort_flag);
+            if (!ok) {
+              part = &v_part[st];
+              break;
+            }
+            parts ^= 1u << st;
+            auto zero = [&](int row, int n) {
+              uint8_t* vt = v_s + st * C::kTileBytes + row * 128;
+              for (int x = lane; x < n * 8; x += 32)
 #pragma unroll
                 for (int ch = 0; ch < C::kChunks; ++ch)
                   *reinterpret_cast<uint4*>(vt + ch * (kKeys * 128) + x * 16) =
                       make_uint4(0, 0, 0, 0);
-              tc::fence_proxy_async();
-              mbar_arrive(&v_tail[st]);
-            }
+            };
+            zero(0, below);
+            zero(z0, nz);
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[st]);
           }
         }
         cta_sync();
       } while (!last);
+      if (part) drain(part, (parts >> (part - v_part)) & 1);
     }
   }
   // (every role has passed its last barrier: no wait is left that could raise the flag)

@@ -3,10 +3,12 @@ import pytest
 import torch
 
 import paged_sparse_kv_sa_b200 as sa
-from test_gpu_dense import check, chunk_case, run_chunk
+from paged_sparse_kv_sa_b200 import workloads as W
+from test_gpu_dense import _cu, _randn, check, chunk_case, run_chunk
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+NAN = float("nan")
 
 
 def test_offsets_that_turn_back_do_not_pass_the_counters():
@@ -40,3 +42,70 @@ def test_queries_that_are_nobodys_change_no_bit(ns, Ls, G, D):
         o, lse, err = run_chunk(c)
         assert err == 0 and torch.equal(o[:sum(ns)], want[0][:sum(ns)])
         assert torch.equal(lse[:sum(ns)], want[1][:sum(ns)])
+
+
+# ------------------------------------------------------------------ behind the window
+BEHIND = [
+    # ns, Ls, G, Hkv, D, P, window
+    ([1], [700], 4, 2, 128, 16, 100),
+    ([1, 90], [5000, 600], 4, 1, 64, 64, 1),
+    ([40, 300], [800, 900], 4, 2, 128, 16, 100),       # items of two full row tiles
+    ([20, 20], [900, 500], 8, 2, 64, 48, 130),
+    ([5, 1], [3000, 290], 4, 2, 128, 256, 333),        # pages larger than a tile
+    ([1] * 40, [1000 + 37 * i for i in range(40)], 4, 2, 64, 16, 129),
+    ([130, 1], [130, 400], 2, 3, 128, 32, 17),         # nothing behind the first one's window
+]
+
+
+def _release(c, ns, P, window, ids):
+    """The keys behind each sequence's window become NaN; ids: the pages that hold nothing
+    else leave the map."""
+    for b, (n, k) in enumerate(zip(ns, c["ks"])):
+        first = max(0, k.shape[0] - n - window + 1)    # the first key that any token sees
+        for p in range(-(-first // P)):
+            ph, m = int(c["pt"][b, p]), min(P, first - p * P)
+            c["kc"][ph, :, :m] = NAN
+            c["vc"][ph, :, :m] = NAN
+            if ids and m == P:
+                c["pt"][b, p] = -1 if p % 2 else 10 ** 7
+
+
+@pytest.mark.parametrize("ids", [False, True])
+@pytest.mark.parametrize("ns,Ls,G,Hkv,D,P,window", BEHIND)
+def test_what_lies_behind_the_window_is_not_looked_at(ns, Ls, G, Hkv, D, P, window, ids):
+    c = chunk_case(60 + sum(Ls), ns, Ls, G, Hkv, D, P)
+    _release(c, ns, P, window, ids)
+    o, lse, err = run_chunk(c, window)
+    assert err == 0
+    check(o, lse, c["q"], c["ks"], c["vs"], ns, c["scale"], window)
+    direc, blocks = W.page_directory(c["pt"], c["sl"], P, 2)
+    e = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o2, lse2 = sa.sa_chunk_attention_dir(c["q"], c["kc"], c["vc"], direc, blocks, 2, c["sl"], c["cu"], c["scale"],
+                                         window=window, dev_error=e)
+    torch.cuda.synchronize()
+    assert int(e.item()) == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_missing_page_inside_the_window_is_still_flagged():
+    ns, Ls, P, window = [4], [900], 16, 200
+    c = chunk_case(61, ns, Ls, 4, 2, 128, P)
+    _release(c, ns, P, window, True)
+    c["pt"][0, 50] = -1                                # keys 800 .. 815
+    o, lse, err = run_chunk(c, window)
+    assert err == 2
+    # the keys of that page are left out: the visible ones around it are the same for a
+    # sequence that never had them, positions and window shortened by a page
+    keep = torch.cat((torch.arange(800), torch.arange(816, 900))).to(DEV)
+    check(o, lse, c["q"], [c["ks"][0][keep]], [c["vs"][0][keep]], ns, c["scale"], window - 16)
+
+
+@pytest.mark.parametrize("n,L,window,D", [(1, 500, 70, 128), (40, 700, 129, 64), (100, 900, 33, 128)])
+def test_packed_keys_behind_the_window_are_not_looked_at(n, L, window, D):
+    g = torch.Generator().manual_seed(L)
+    q, k, v = _randn(g, n, 8, D), _randn(g, L, 2, D), _randn(g, L, 2, D)
+    k2, v2 = k.clone(), v.clone()
+    k2[:L - n - window + 1] = NAN
+    v2[:L - n - window + 1] = NAN
+    o, lse = sa.sa_prompt_attention(q, k2, v2, _cu([n]), _cu([L]), 0.1, window=window)
+    torch.cuda.synchronize()
+    check(o, lse, q, [k], [v], [n], 0.1, window)
