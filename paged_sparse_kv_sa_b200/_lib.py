@@ -938,6 +938,12 @@ def _dense_workspace(total_q, Hq, Hkv, D, device, stream):
     return _empty(max(n, 16), torch.uint8, device, stream)
 
 
+def _window(window) -> int:
+    """The window as the C call's 32-bit argument: a longer one is every earlier key (sequences
+    stay below 2^30 keys), and one below 0 stays there and is refused."""
+    return max(-1, min(window, 0x7fffffff))
+
+
 def _dense_outputs(q, shape, Hkv, o_out, lse_out, workspace, dev_error, stream):
     """The outputs and workspace of a dense call, made where they are not given."""
     if not q.is_cuda:
@@ -985,7 +991,7 @@ def _chunk(q, k_cache, v_cache, page_map, seq_lens, cu_q, scale, window, o_out, 
     pq, pcu, pk, pv, pm, pb, psl, po, pl, pw, pe = _ptrs(
         dev, q, cu_q, k_cache, v_cache, page_map[0], None if flat else page_map[1], seq_lens,
         o_out, lse_out, workspace, dev_error)
-    rest = (psl, B, Hq, Hkv, D, P, P_pool, scale, window, po, pl, pw, workspace.numel(), pe,
+    rest = (psl, B, Hq, Hkv, D, P, P_pool, scale, _window(window), po, pl, pw, workspace.numel(), pe,
             _raw_stream(stream, dev))
     head = (pq, _stride_array(q), pcu, total, pk, _stride_array(k_cache), pv,
             _stride_array(v_cache), pm, n_map)
@@ -1039,7 +1045,7 @@ def sa_prompt_attention(q, k, v, cu_q, cu_k, scale: float, window: int = 0, o_ou
                                                  workspace, dev_error)
     _call(lib.sa_prompt_attention,
           (pq, _stride_array(q), pcu, total, pk, _stride_array(k), pv, _stride_array(v), pck,
-           total_k, B, Hq, Hkv, D, scale, window, po, pl, pw, workspace.numel(), pe,
+           total_k, B, Hq, Hkv, D, scale, _window(window), po, pl, pw, workspace.numel(), pe,
            _raw_stream(stream, dev)), "sa_prompt_attention")
     return o_out, lse_out
 

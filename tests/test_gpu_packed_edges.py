@@ -109,3 +109,23 @@ def test_packed_keys_behind_the_window_are_not_looked_at(n, L, window, D):
     o, lse = sa.sa_prompt_attention(q, k2, v2, _cu([n]), _cu([L]), 0.1, window=window)
     torch.cuda.synchronize()
     check(o, lse, q, [k], [v], [n], 0.1, window)
+
+
+# ------------------------------------------------------------------ windows past 32 bits
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 40 + 7])
+def test_windows_past_32_bits_are_no_limit(window):
+    c = chunk_case(62, [3], [300], 4, 2, 64, 16)
+    want, want_lse, _ = run_chunk(c)
+    o, lse, _ = run_chunk(c, window)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    q, k, v = c["q"], c["ks"][0], c["vs"][0]
+    a = sa.sa_prompt_attention(q, k, v, _cu([3]), _cu([300]), 0.1)
+    b = sa.sa_prompt_attention(q, k, v, _cu([3]), _cu([300]), 0.1, window=window)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("window", [-1, -2 ** 32 + 5, -2 ** 40])
+def test_negative_windows_are_refused(window):
+    c = chunk_case(62, [3], [300], 4, 2, 64, 16)
+    with pytest.raises(sa.SAError):
+        run_chunk(c, window)
