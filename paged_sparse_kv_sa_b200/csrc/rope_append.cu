@@ -154,8 +154,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppe
     const int b = last_le(a.B, t, [&](int i) { return (int64_t)a.cu[i]; });
     const int t0 = a.cu[b], t1 = a.cu[b + 1], L = a.seq_lens[b];
     const int64_t i = (int64_t)t - t0;
-    // no sequence's token (or one whose offsets or length its page CTAs flag)
-    if (t0 < 0 || i < 0 || t >= t1 || t1 > a.total || L < 0) return;
+    // no sequence's token, or one of a sequence that is skipped (offsets, length)
+    if (t0 < 0 || i < 0 || t >= t1 || t1 > a.total || L < 0 ||
+        L > (int64_t)a.max_pages * a.P)
+      return;
     const int64_t pos = L + i;
     if (pos >= a.n_pos) {
       if (lane == 0) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);

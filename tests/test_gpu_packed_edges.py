@@ -1,10 +1,12 @@
 """Edges of the packed-batch operators (marked gpu)."""
+import numpy as np
 import pytest
 import torch
 
 import paged_sparse_kv_sa_b200 as sa
 from paged_sparse_kv_sa_b200 import workloads as W
 from test_gpu_dense import _cu, _randn, check, chunk_case, run_chunk
+from test_gpu_rope_append import _bits, _case, _gpu, _i32, _run, _want
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -129,3 +131,28 @@ def test_negative_windows_are_refused(window):
     c = chunk_case(62, [3], [300], 4, 2, 64, 16)
     with pytest.raises(sa.SAError):
         run_chunk(c, window)
+
+
+# ------------------------------------------------------------------ appends that skip
+def _long_table(n):
+    f = np.arange(n)[:, None] * 10000.0 ** (-np.arange(0, 64, 2) / 64)
+    return torch.from_numpy(np.concatenate((np.cos(f), np.sin(f)), 1).astype(np.float32)).to(DEV)
+
+
+def test_a_length_past_the_page_map_skips_the_sequence_and_its_queries():
+    c = _case(70, [6, 3], [0, 5], 4, 2, 64, 16, 64)
+    cap = c["pt"].shape[1] * 16
+    for bad in (cap + 1, cap + 40, 2 ** 30):
+        d = dict(_gpu(c), sl=_i32([bad, 5]), table=_long_table(500))
+        before = {k: d[k].clone() for k in ("kc", "vc", "sig")}
+        qo = torch.full_like(d["q"], 7.0)
+        qo, new, err = _run(d, q_out=qo)
+        assert err & 1 and bool((qo[:6] == 7).all())
+        q, _, kc, vc, sig, _ = _want(dict(c, q=c["q"][6:], k=c["k"][6:], v=c["v"][6:], cu=np.array([0, 3]),
+                                          pt=c["pt"][1:], sl=c["sl"][1:]))
+        assert np.array_equal(_bits(qo)[6:], q)
+        mine = int(c["pt"][1, 0])
+        for k, x in (("kc", kc), ("vc", vc), ("sig", sig)):
+            assert np.array_equal(_bits(d[k])[mine], x[mine])
+            rest = torch.arange(d[k].shape[0], device=DEV) != mine
+            assert torch.equal(d[k][rest].view(torch.int16), before[k][rest].view(torch.int16))
