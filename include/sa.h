@@ -624,7 +624,8 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  * written.  An offset that breaks this is flagged (SA_DEVERR_COUNT): the
  * attention calls then hold it inside the tensors (what such a sequence's rows
  * receive is unspecified; where offsets turn back, so that sequences share
- * tokens, what any row receives, if anything), the append skips the sequence.
+ * tokens, what any row receives, if anything), the append skips the sequence
+ * (where offsets turn back, tokens that sequences share may be appended in part).
  * Strides are three (token, head, feature), with the rules of every bf16
  * tensor (feature 1, the others multiples of 8, base 16-byte aligned).
  */
@@ -644,6 +645,8 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  * query to q_out.  Then, for every page the tokens fall in, summaries[page, g]
  * becomes the mean of the page's stored keys at positions below seq_lens[b] +
  * n_b, as sa_build_page_summaries computes it.  No other row changes.
+ * A sequence whose length is below 0 or past the page table's row is skipped, its
+ * queries too, and flagged (SA_DEVERR_PAGE_RANGE).
  * Positions past the page table's row or at or past n_pos are dropped and
  * flagged (SA_DEVERR_PAGE_RANGE; a query past n_pos is not written either);
  * tokens whose page id is out of range likewise (SA_DEVERR_POOL_RANGE).
@@ -655,11 +658,13 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  *             cosines, then sines (NULL when rot_dim == 0: a plain append)
  *  q_out      (dev) [total_new,Hq,D] bf16, contiguous; may be q_new itself
  *  k_out      (dev, optional) [total_new,Hkv,D] bf16, contiguous: the rotated
- *             keys, packed (for sa_prompt_attention); may be k_new itself
+ *             keys, packed (for sa_prompt_attention); may be k_new itself; rows
+ *             of tokens that are not appended are left as they were
  *  k_cache, v_cache (dev) [P_pool,Hkv,P,D] bf16, written in place
  *  seq_lens   (dev) [B] int32: the lengths BEFORE the append
- *  out_seq_lens (dev, optional) [B] int32: receives seq_lens[b] + n_b; must not
- *             be seq_lens itself
+ *  out_seq_lens (dev, optional) [B] int32: receives seq_lens[b] + n_b (tokens
+ *             dropped past an end counted), or seq_lens[b] of a sequence that is
+ *             skipped; must not be seq_lens itself
  *  summaries  (dev, optional) [P_pool,Hkv,D] bf16, contiguous
  * D % 8 == 0, D <= 256; rot_dim % 16 == 0, rot_dim <= D; max_pages * page_size
  * + total_new and page_size * D below 2^31 (SA_ERR_UNSUPPORTED otherwise).

@@ -188,6 +188,23 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppe
     }
     return;
   }
+  const int64_t cap = (int64_t)a.max_pages * a.P;
+  // ================= every sequence's length, and what is wrong with it: one thread per
+  // sequence, whether or not its page slots can be found, in the last page CTAs (their
+  // slots are the likeliest to be nobody's)
+  if (a.page_ctas - 1 - blockIdx.x <= (a.B - 1) / kThreads) {
+    const int b = (a.page_ctas - 1 - blockIdx.x) * kThreads + tid;
+    if (b < a.B) {
+      const int t0 = a.cu[b], t1 = a.cu[b + 1], L = a.seq_lens[b];
+      const bool bad_cu = t0 < 0 || t1 < t0 || t1 > a.total, bad_len = L < 0 || L > cap;
+      const int n = bad_cu || bad_len ? 0 : t1 - t0;
+      if (a.out_seq_lens) a.out_seq_lens[b] = L + n;
+      if (bad_cu) set_dev_error(a.err, SA_DEVERR_COUNT);
+      const int64_t end = (int64_t)L + n;
+      if (bad_len || (n > 0 && (end > cap || end > a.n_pos)))
+        set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
+    }
+  }
   // ================= one touched page of one kv head
   __shared__ __align__(16) uint16_t key_s[kStage];   // a block of rows of keys
   __shared__ double sum_s[kThreads];                 // [row group][column]
@@ -197,25 +214,12 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppe
   const int hn = min(a.page_heads, a.Hkv - h0);
   const int P = a.P;
   const int b = last_le(a.B, s, [&](int i) { return (int64_t)(a.cu[i] / P) + 2 * i; });
-  const bool lead = tid == 0 && h0 == 0;
   const int t0 = a.cu[b], t1 = a.cu[b + 1], L = a.seq_lens[b];
   const int j = s - (t0 / P + 2 * b);
-  if (t0 < 0 || t1 < t0 || t1 > a.total) {
-    if (lead) set_dev_error(a.err, SA_DEVERR_COUNT);
-    return;
-  }
-  const int64_t cap = (int64_t)a.max_pages * P;
-  if (L < 0 || L > cap) {
-    if (lead) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
-    return;
-  }
+  if (t0 < 0 || t1 < t0 || t1 > a.total || L < 0 || L > cap) return;   // (flagged above)
   const int n = t1 - t0;
-  if (j == 0 && lead && a.out_seq_lens) a.out_seq_lens[b] = L + n;
   int64_t end = (int64_t)L + n;
-  if (end > cap || end > a.n_pos) {   // tokens past the page map or the table are dropped
-    if (lead && j == 0 && n > 0) set_dev_error(a.err, SA_DEVERR_PAGE_RANGE);
-    end = cap < a.n_pos ? cap : a.n_pos;
-  }
+  if (end > cap || end > a.n_pos) end = cap < a.n_pos ? cap : a.n_pos;   // the rest is dropped
   const int64_t p = L / P + j, p0 = p * P;
   if (j < 0 || end <= L || p0 >= end) return;
   const int ph = page_at(a.pt, b, (int)p);

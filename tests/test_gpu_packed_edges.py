@@ -156,3 +156,41 @@ def test_a_length_past_the_page_map_skips_the_sequence_and_its_queries():
             assert np.array_equal(_bits(d[k])[mine], x[mine])
             rest = torch.arange(d[k].shape[0], device=DEV) != mine
             assert torch.equal(d[k][rest].view(torch.int16), before[k][rest].view(torch.int16))
+
+
+@pytest.mark.parametrize("lens,cu,want", [
+    ([-4, 5], [0, 20, 23], [-4, 8]),            # a negative length
+    ([5000, 5], [0, 20, 23], [5000, 8]),        # one past the page map
+    ([0, 5], [-5, 20, 23], [0, 8]),             # offsets outside the tokens
+    ([0, 5], [0, 20, 5000], [20, 5]),
+    ([0, 5], [0, -1, 23], [0, 5]),              # offsets that turn back
+    ([30, 5], [0, 20, 23], [50, 8]),            # tokens past the page map: counted, flagged
+])
+def test_every_sequence_reports_its_length(lens, cu, want):
+    c = _case(71, [20, 3], [0, 5], 4, 2, 64, 16, 64)
+    d = dict(_gpu(c), sl=_i32(lens), cu=_i32(cu))
+    _, new, err = _run(d)
+    assert err != 0 and new.tolist() == want
+
+
+def test_lengths_of_many_sequences():
+    # more sequences than one block reports, good and bad ones mixed
+    B = 700
+    rng = np.random.default_rng(2)
+    ns = [int(x) for x in rng.integers(0, 3, B)]
+    c = _case(72, ns, [int(x) for x in rng.integers(0, 20, B)], 2, 1, 64, 16, 64)
+    d = _gpu(c)
+    _, new, err = _run(d)
+    assert err == 0 and np.array_equal(new.cpu().numpy(), _want(c)[5])
+    sl = c["sl"].copy()
+    sl[::97] = -1
+    want = np.where(sl < 0, sl, sl + np.array(ns))
+    _, new, err = _run(dict(_gpu(c), sl=_i32(sl)))
+    assert err & 1 and np.array_equal(new.cpu().numpy(), want)
+
+
+def test_offsets_that_turn_back_are_flagged_wherever_they_do():
+    # the tokens of the sequence between do not exist, and its page slots are another's
+    c = _case(73, [100, 10, 90], [0, 0, 0], 2, 1, 64, 16, 64)
+    _, new, err = _run(dict(_gpu(c), cu=_i32([0, 100, 50, 200])))
+    assert err & 4 and int(new[1]) == 0
