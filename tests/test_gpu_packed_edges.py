@@ -1,11 +1,14 @@
 """Edges of the packed-batch operators (marked gpu)."""
+import ctypes
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import paged_sparse_kv_sa_b200 as sa
 from paged_sparse_kv_sa_b200 import workloads as W
-from test_gpu_dense import _cu, _randn, check, chunk_case, run_chunk
+from test_gpu_dense import U, _cu, _randn, check, chunk_case, run_chunk
 from test_gpu_rope_append import _bits, _case, _gpu, _i32, _run, _want
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +197,45 @@ def test_offsets_that_turn_back_are_flagged_wherever_they_do():
     c = _case(73, [100, 10, 90], [0, 0, 0], 2, 1, 64, 16, 64)
     _, new, err = _run(dict(_gpu(c), cu=_i32([0, 100, 50, 200])))
     assert err & 4 and int(new[1]) == 0
+
+
+# ------------------------------------------------------------------ the optional LSE, the largest batch
+def test_without_an_lse():
+    c = chunk_case(63, [1, 30, 300], [2000, 500, 700], 4, 2, 128, 16)
+    want, _, _ = run_chunk(c)
+    q, o = c["q"], torch.empty_like(c["q"])
+    ws = sa.dense_attention_workspace(q.shape[0], 8, 2, 128, DEV)
+    s3, s4 = (lambda t: (ctypes.c_int64 * 3)(*t.stride())), (lambda t: (ctypes.c_int64 * 4)(*t.stride()))
+    lib, st = sa.load(), torch.cuda.current_stream().cuda_stream
+    assert lib.sa_chunk_attention(q.data_ptr(), s3(q), c["cu"].data_ptr(), q.shape[0], c["kc"].data_ptr(), s4(c["kc"]),
+                                  c["vc"].data_ptr(), s4(c["vc"]), c["pt"].data_ptr(), c["pt"].shape[1],
+                                  c["sl"].data_ptr(), 3, 8, 2, 128, 16, c["kc"].shape[0], c["scale"], 0, o.data_ptr(),
+                                  None, ws.data_ptr(), ws.numel(), None, st) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+
+
+def test_the_largest_batch():
+    B, L, D, P = 4096, 20, 64, 32
+    g = torch.Generator().manual_seed(9)
+    rng = np.random.default_rng(3)
+    ns = [int(x) for x in rng.integers(0, 2, B)]
+    q, kc, vc = _randn(g, sum(ns), 2, D), _randn(g, B, 1, P, D), _randn(g, B, 1, P, D)
+    pt = torch.randperm(B, generator=g).to(torch.int32).to(DEV).view(B, 1)
+    sl = torch.from_numpy(rng.integers(1, L + 1, B).astype(np.int32)).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = sa.sa_chunk_attention(q, kc, vc, pt, sl, _cu(ns), 0.125, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    b = torch.tensor([i for i, n in enumerate(ns) if n], device=DEV)
+    k, v = (x[pt[b, 0].long(), 0].double() for x in (kc, vc))
+    hide = torch.arange(P, device=DEV)[None, :] >= sl[b][:, None]
+    s = 0.125 * torch.einsum("bhd,bld->bhl", q.double(), k)
+    reach = 0.125 * torch.einsum("bhd,bld->bhl", q.double().abs(), k.abs()).masked_fill(hide[:, None], 0.0).amax(-1)
+    s = s.masked_fill(hide[:, None], -math.inf)
+    w = torch.softmax(s, -1)
+    A, ref = torch.einsum("bhl,bld->bhd", w, v.abs()), torch.einsum("bhl,bld->bhd", w, v)
+    eta = (D + 4) * 2.0 ** -23 * reach + 2.0 ** -21        # the bounds of test_gpu_dense.py
+    assert bool(((o.double() - ref).abs() <= U * (A + ref.abs()) * (1 + U) + 4 * eta[..., None] * A).all())
+    z = torch.logsumexp(s, -1)
+    assert bool(((lse.double() - z).abs() <= eta + 21 * 2.0 ** -24 + 2.0 ** -22 * z.abs()).all())
