@@ -708,7 +708,8 @@ SA_API int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[
  *  page_table (dev) [B,max_pages] int32;  seq_lens (dev) [B] int32
  *  scale      finite, above 0
  *  window     0 (every earlier key) or the number of keys a token sees
- *  o_out      (dev) [total_q,Hq,D] bf16, contiguous, 16-byte aligned
+ *  o_out      (dev) [total_q,Hq,D] bf16, contiguous, 16-byte aligned; must not
+ *             overlap q, k or v (SA_ERR_INVALID_ARG where it is one of them)
  *  lse_out    (dev, optional) [total_q,Hq] float32
  *  workspace  (dev) sa_dense_attention_workspace_size(total_q,Hq,Hkv,D) bytes,
  *             16-byte aligned, caller-owned, no initial contents; calls (or

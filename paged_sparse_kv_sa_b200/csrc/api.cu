@@ -1311,6 +1311,7 @@ int chunk_impl(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int to
   a.P = page_size;
   a.P_pool = P_pool;
   if (!dense_countable(a, (int64_t)max_pages * page_size)) return SA_ERR_UNSUPPORTED;
+  if (o == q || o == k_cache || o == v_cache) return SA_ERR_INVALID_ARG;   // read while it is written
   a.box = 16;
   while (a.box < 128 && page_size % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap qmap, kmap, vmap;
@@ -1415,6 +1416,7 @@ int sa_prompt_attention(const uint16_t* q, const int64_t q_strides[3], const int
       return SA_ERR_UNSUPPORTED;
   }
   if (!dense_countable(a, total_k)) return SA_ERR_UNSUPPORTED;
+  if (o_out == q || o_out == k || o_out == v) return SA_ERR_INVALID_ARG;
   a.cu_k = cu_k;
   a.total_k = total_k;
   a.P = 128;
