@@ -620,8 +620,9 @@ SA_API int sa_append_kv_dir(const uint16_t* k_new, const int64_t kn_strides[4],
  * end to end: sequence b owns the tokens cu[b] .. cu[b + 1] - 1 (n_b of them,
  * any number, none included) of [tokens, heads, D] tensors, cu being B + 1
  * non-decreasing device int32 offsets with cu[0] >= 0 and cu[B] <= the number
- * of tokens the call is given.  Tokens behind cu[B] are neither read nor
- * written.  An offset that breaks this is flagged (SA_DEVERR_COUNT): the
+ * of tokens the call is given.  Tokens before cu[0] or behind cu[B] are not
+ * written and change nothing (the attention calls may load them beside others).
+ * An offset that breaks this is flagged (SA_DEVERR_COUNT): the
  * attention calls then hold it inside the tensors (what such a sequence's rows
  * receive is unspecified; where offsets turn back, so that sequences share
  * tokens, what any row receives, if anything), the append skips the sequence

@@ -1023,7 +1023,7 @@ cudaError_t launch_d(const DenseArgs& a, const CUtensorMap& qmap, const CUtensor
   if (e != cudaSuccess) return e;
   // the merge is launched under the first kernel's tail (it waits for its end); a
   // warp does one row where rows are few, two where they are many (four, in blocks
-  // of 32 warps: 16 x 32K-key decode 358 us, so 354)
+  // of 32 warps: 16 x 32K-key decode 358 us, so 354, each in a burst of replays)
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -19,8 +19,9 @@
 // and then sums each column in float64 from there (one column per thread: few
 // registers, so enough CTAs are resident to keep the loads in flight; 8254 tokens
 // with the sums kept per thread while loading 109 us, with one column per thread
-// 65, with several heads per CTA 45, with two heads in flight 41; 208 MB, so 5.1
-// TB/s).  A query CTA rotates the heads of a few tokens, one warp per token: a
+// 65, with several heads per CTA 45, with two heads in flight 41, all as graph
+// replays; 208 MB, so 5.1 TB/s, and 4.8 in the 43 us of a call among others).  One
+// thread per sequence reports its new length and bad offsets.  A query CTA rotates the heads of a few tokens, one warp per token: a
 // lane keeps its unit of the head, so it reads its cosines and sines once for all
 // heads.  Page slots and tokens find their sequence by a 32-way search of the
 // offsets: slot s belongs to the last b with floor(cu[b]/P) + 2b <= s (n tokens

@@ -19,6 +19,7 @@ DEV = "cuda"
 def hasty(tmp_path_factory):
     """The library with dense.cu rebuilt for waits of 8 polls that do not suspend."""
     d = str(tmp_path_factory.mktemp("hasty"))
+    os.makedirs(build.OBJ, exist_ok=True)
     objs = [build._compile(s, False) for s in build.SOURCES if s != "dense.cu"]
     objs.append(build._compile("dense.cu", True, d, ("SA_DENSE_POLLS=8",)))
     out = os.path.join(d, "libsa_hasty.so")
