@@ -707,7 +707,7 @@ SA_API int sa_append_kv_rope_dir(const uint16_t* q_new, const int64_t q_strides[
  *  q          (dev) [total_q,Hq,D] bf16;  cu_q (dev) [B+1] int32
  *  k_cache, v_cache (dev) [P_pool,Hkv,P,D] bf16, strides as sa_sparse_decode
  *  page_table (dev) [B,max_pages] int32;  seq_lens (dev) [B] int32
- *  scale      finite, above 0
+ *  scale      above 0; scale * log2(e) finite
  *  window     0 (every earlier key) or the number of keys a token sees
  *  o_out      (dev) [total_q,Hq,D] bf16, contiguous, 16-byte aligned; must not
  *             overlap q, k or v (SA_ERR_INVALID_ARG where it is one of them)

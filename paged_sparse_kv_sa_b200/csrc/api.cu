@@ -1256,8 +1256,9 @@ bool dense_countable(const DenseArgs& a, int64_t max_len) {
 int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int total_q, int B,
                  int Hq, int Hkv, int D, float scale, int window, uint16_t* o, float* lse,
                  void* workspace, size_t workspace_bytes, int32_t* dev_error, DenseArgs* a) {
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   if (B < 0 || total_q < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || window < 0 ||
-      !std::isfinite(scale) || !(scale > 0.f))
+      !std::isfinite(scale_log2) || !(scale_log2 > 0.f))
     return SA_ERR_INVALID_ARG;
   if (B == 0 || total_q == 0) return SA_OK;
   if (int r = check_packed(q, qs)) return r;
@@ -1279,7 +1280,7 @@ int dense_common(const uint16_t* q, const int64_t* qs, const int32_t* cu_q, int 
   a->D = D;
   a->tile_toks = dense_tile_toks(Hq / Hkv);
   a->window = window < (1 << 30) ? window : 0;   // positions stay below 2^30
-  a->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  a->scale_log2 = scale_log2;
   a->o = o;
   a->lse = lse;
   a->err = dev_error;

@@ -19,3 +19,10 @@ def test_dense_attention_refuses_an_output_that_is_an_input():
         assert _call("sa_chunk_attention", CHUNK, **kw) == INVALID
         assert _call("sa_prompt_attention", PROMPT, **kw) == INVALID
     assert _call("sa_prompt_attention", PROMPT) == INVALID
+
+
+def test_dense_attention_refuses_a_scale_whose_base_2_form_is_infinite():
+    for name, base in (("sa_chunk_attention", CHUNK), ("sa_prompt_attention", PROMPT)):
+        for scale in (2.4e38, 3.4e38):
+            assert _call(name, base, scale=scale, q=OTHER, k=OTHER, v=OTHER, total=1 << 28) == INVALID
+        assert _call(name, base, scale=2.3e38, total=1 << 28) == UNSUPPORTED   # the next check's
