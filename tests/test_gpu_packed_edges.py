@@ -239,3 +239,25 @@ def test_the_largest_batch():
     assert bool(((o.double() - ref).abs() <= U * (A + ref.abs()) * (1 + U) + 4 * eta[..., None] * A).all())
     z = torch.logsumexp(s, -1)
     assert bool(((lse.double() - z).abs() <= eta + 21 * 2.0 ** -24 + 2.0 ** -22 * z.abs()).all())
+
+
+def test_pages_past_32_bits_of_elements():
+    # the last pages of a pool of more than 2^31 elements: appended to, then attended over
+    Hq, Hkv, P, D, n = 16, 8, 16, 128, 100
+    pool = (1 << 31) // (Hkv * P * D) + 10
+    kc, vc = (torch.empty((pool, Hkv, P, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    sig = torch.empty((pool, Hkv, D), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (_randn(g, n, h, D) for h in (Hq, Hkv, Hkv))
+    pt = (pool - 1 - torch.arange(7, dtype=torch.int32, device=DEV)).view(1, 7).contiguous()
+    table, k_out, lens = _long_table(n), torch.empty_like(k), torch.empty(1, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qo, _ = sa.sa_append_kv_rope(q, k, v, _cu([n]), table, kc, vc, pt, _i32([0]), sig, k_out=k_out, out_seq_lens=lens,
+                                 dev_error=err)
+    o, lse = sa.sa_chunk_attention(qo, kc, vc, pt, lens, _cu([n]), 0.09, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and lens.tolist() == [n]
+    rows = kc[pt[0].long()].transpose(1, 2).reshape(-1, Hkv, D)[:n]
+    assert torch.equal(rows, k_out) and torch.equal(vc[pt[0].long()].transpose(1, 2).reshape(-1, Hkv, D)[:n], v)
+    assert torch.equal(sig[pt[0, 0].long()], k_out[:P].double().mean(0).to(torch.bfloat16))
+    check(o, lse, qo, [k_out], [v], [n], 0.09, 0)
